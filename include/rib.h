@@ -412,6 +412,83 @@ rib_status rib_f32_to_bf16(const float* x, void* y, size_t n, cudaStream_t strea
  * x 8-byte and y 16-byte aligned; n == 0 launches nothing. */
 rib_status rib_bf16_to_f32(const void* x, float* y, size_t n, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Training-block operators: the join of a block with its residual stream,
+ * dropout, and differential attention. They stand beside rib_layernorm and
+ * rib_window_attention and follow the conventions above; every call may be
+ * captured into a CUDA graph, and none keeps anything between calls.
+ * ---------------------------------------------------------------------- */
+
+/* Dropout with a mask that is never stored: y[i] = x[i] / keep where the
+ * element's 16 random bits reach round(65536 p), else 0 (whatever x[i] is);
+ * keep = 1 - round(65536 p) / 65536. The bits are those of Philox4x32-10
+ * (Salmon et al., "Parallel random numbers: as easy as 1, 2, 3", SC 2011) at
+ * counter words (i / 8 low, i / 8 high, offset low, offset high) and key
+ * `seed`: element i takes half (i % 2) of output word (i % 8) / 2. They depend
+ * on i, seed and offset alone, so the backward is the same call on the
+ * upstream gradient. step: device word (8-byte aligned) added to offset when
+ * the kernel runs, or NULL; a captured graph draws new masks at each replay
+ * when the program advances it. x and y hold n values of dtype (RIB_BF16,
+ * RIB_F32 or RIB_F16); y may be x, but may not overlap it otherwise. n <= 2^42;
+ * n == 0 launches nothing. 0 <= p <= 1 (1 drops everything). Values are not
+ * clamped: an fp16 overflow becomes infinity, which loss scaling looks for. */
+rib_status rib_dropout(const void* x, void* y, rib_dtype dtype, size_t n, float p, uint64_t seed, uint64_t offset,
+                       const uint64_t* step, cudaStream_t stream);
+
+typedef enum { RIB_NORM_NONE = 0, RIB_NORM_LAYER = 1, RIB_NORM_RMS = 2 } rib_norm;
+
+/* The join of a block with its residual stream, with the norms on both sides:
+ *   u  = N_post(y) post_w + post_b         (y itself with RIB_NORM_NONE)
+ *   x' = x + dropout(scale[group] * gate * u)
+ *   h  = N_pre(x') pre_w + pre_b           (the next block's input)
+ * N(v) is (v - mean) / sqrt(var + eps) over the C values of a row
+ * (RIB_NORM_LAYER, biased variance) or v / sqrt(mean(v^2) + eps)
+ * (RIB_NORM_RMS). Statistics, products and sums are fp32. */
+typedef struct {
+  long long T;              /* rows (tokens) */
+  int C;                    /* values of a row, 1..4096 */
+  long long rows_per_group; /* rows that share a row of scale: T for one
+                               residual scale, H*W for one per image. At most
+                               1024 groups; the last may be shorter */
+  rib_dtype x_dtype;        /* x, x_out, dx_out, dx: RIB_F32, or dtype */
+  rib_dtype dtype;          /* y, gate, h, dh, dy, dgate */
+  rib_norm pre, post;
+  float eps;                /* > 0, of both norms */
+  float p;                  /* dropout of the branch, rib_dropout's mask for
+                               element row * C + column; 0: none */
+  uint64_t seed, offset;
+} rib_residual_norm_desc;
+
+/* Forward. x, y, gate, x_out, h: contiguous [T][C]. scale fp32 [groups][C];
+ * post_w, post_b, pre_w, pre_b fp32 [C]; each may be NULL (1 and 0), as may
+ * gate. y NULL: no branch (x' = x, h alone is written; x_out must be NULL).
+ * x_out NULL: x' is not stored. h goes with pre != RIB_NORM_NONE. x_out may be
+ * x, and h may be y. h is taken from x' before x' is rounded to x_dtype. fp16
+ * results saturate at +-65504. T == 0 launches nothing. Tensors need their
+ * element's alignment; with C % 4 == 0 and every tensor aligned to four
+ * elements the rows move as vectors. */
+rib_status rib_residual_norm(const rib_residual_norm_desc* desc, const void* x, const void* y, const void* gate,
+                             const float* scale, const float* post_w, const float* post_b, const float* pre_w,
+                             const float* pre_b, void* x_out, void* h, const uint64_t* step, cudaStream_t stream);
+
+/* Backward. x_out, y, gate, scale, post_w, post_b, pre_w, step and desc as in
+ * the forward (x_out its output; x itself when y is NULL); dx_out: gradient of
+ * x_out from the stream, NULL for none; dh: gradient of h (with a pre norm).
+ * Statistics are recomputed; from a 16-bit x_out they are those of the rounded
+ * values. Outputs, each NULL when not wanted: dx (gradient of x), dy, dgate
+ * [T][C]; dscale fp32 [groups][C]; dpost_w, dpost_b, dpre_w, dpre_b fp32 [C].
+ * All overwritten. dx may be dx_out, dy may be y or dh, dgate may be gate. The
+ * weight gradients need workspace >= rib_residual_norm_bwd_workspace_size()
+ * bytes, 4-byte aligned; they are sums of per-CTA partials added in a fixed
+ * order, the same bits on every run. T == 0 writes zero weight gradients (and
+ * no dscale, which has no rows). Gradients are not clamped. */
+size_t rib_residual_norm_bwd_workspace_size(const rib_residual_norm_desc* desc);
+rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* desc, const void* x_out, const void* y, const void* gate,
+                                 const float* scale, const float* post_w, const float* post_b, const float* pre_w,
+                                 const void* dx_out, const void* dh, void* dx, void* dy, void* dgate, float* dscale,
+                                 float* dpost_w, float* dpost_b, float* dpre_w, float* dpre_b, void* workspace,
+                                 size_t workspace_bytes, const uint64_t* step, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -13,6 +13,8 @@ from ._lib import (  # noqa: F401
     rib_qkv_project_bwd, cla_gate_bwd, cla_gate_bwd_workspace_size, rib_qkv_project_bwd_workspace_size,
     rib_selftest_wait_timeout, rib_selftest_mma_rate, v_dtype,
     rib_conv_ffn, rib_conv_ffn_workspace_size,
+    ResidualNormDesc, residual_norm_desc, rib_dropout, rib_residual_norm, rib_residual_norm_bwd,
+    rib_residual_norm_bwd_workspace_size,
 )
 from .workloads import WORKLOADS, LayerShape, Workload, make_inputs  # noqa: F401
 

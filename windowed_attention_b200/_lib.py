@@ -56,6 +56,12 @@ class AttnDesc(ctypes.Structure):
                 ("softmax_scale", ctypes.c_float), ("mask_padding", ctypes.c_int), ("out_dtype", ctypes.c_int)]
 
 
+class ResidualNormDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_longlong), ("C", ctypes.c_int), ("rows_per_group", ctypes.c_longlong),
+                ("x_dtype", ctypes.c_int), ("dtype", ctypes.c_int), ("pre", ctypes.c_int), ("post", ctypes.c_int),
+                ("eps", ctypes.c_float), ("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -88,6 +94,10 @@ _SIGNATURES = {
     "rib_selftest_mma_rate": ([_i, _i, _i, _i, _vp, _vp, _vp], _i),
     "rib_conv_ffn_workspace_size": ([_i, _i, _i, _i], _sz),
     "rib_conv_ffn": ([_vp, _i, _vp, _i, _i, _i, _i, _i] + [_vp] * 7 + [_sz, _vp], _i),
+    "rib_dropout": ([_vp, _vp, _i, _sz, _f, ctypes.c_uint64, ctypes.c_uint64, _vp, _vp], _i),
+    "rib_residual_norm": ([ctypes.POINTER(ResidualNormDesc)] + [_vp] * 12, _i),
+    "rib_residual_norm_bwd_workspace_size": ([ctypes.POINTER(ResidualNormDesc)], _sz),
+    "rib_residual_norm_bwd": ([ctypes.POINTER(ResidualNormDesc)] + [_vp] * 18 + [_sz, _vp, _vp], _i),
 }
 
 
@@ -360,3 +370,126 @@ def rib_conv_ffn(xn, x, B, H, W, C, hidden, W1, b1, Wf, bf, W2, b2, workspace, s
     _check(_lib.rib_conv_ffn(_ptr(xn), _dtype_code(xn), _ptr(x), B, H, W, C, hidden, _ptr(W1), _ptr(b1), _ptr(Wf),
                              _ptr(bf), _ptr(W2), _ptr(b2), _ptr(workspace), workspace.numel() * workspace.element_size(),
                              _stream(stream)))
+
+
+# ------------------------------------------------- training-block operators
+# These calls check what the C interface cannot see: that every tensor is on
+# the current device (the kernels run there), has its type and holds enough.
+_NORMS = {"none": 0, "layer": 1, "rms": 2}
+_TORCH_CODE = {}
+
+
+def _code(dtype) -> int:
+    """RIB_* code of a torch dtype; anything but bf16, fp32 and fp16 is refused."""
+    if not _TORCH_CODE:
+        import torch
+        _TORCH_CODE.update({torch.bfloat16: RIB_BF16, torch.float32: RIB_F32, torch.float16: RIB_F16})
+    try:
+        return _TORCH_CODE[dtype]
+    except KeyError:
+        raise ValueError(f"dtype {dtype}: librib takes bfloat16, float32 and float16") from None
+
+
+def _current_device(t) -> int:
+    import torch
+    if not t.is_cuda:
+        raise ValueError("librib entry points take device tensors")
+    d = torch.cuda.current_device()
+    if t.device.index != d:
+        raise ValueError(f"tensor on {t.device} while the current device is cuda:{d}: make its device current for the call")
+    return d
+
+
+def _arg(name, t, numel, code, device) -> Optional[int]:
+    """Pointer of a contiguous device tensor of at least `numel` values of type `code`; None stays None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
+    if _code(t.dtype) != code:
+        raise ValueError(f"{name} is {t.dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} holds {t.numel()} values, {numel} are needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: librib entry points take contiguous tensors")
+    return t.data_ptr()
+
+
+def _step_arg(step, device) -> Optional[int]:
+    """Pointer of the device word added to a dropout offset."""
+    import torch
+    if step is None:
+        return None
+    if step.dtype not in (torch.int64, torch.uint64) or step.numel() < 1 or not step.is_cuda or step.device.index != device:
+        raise ValueError("step is one int64 or uint64 on the current device")
+    return step.data_ptr()
+
+
+def rib_dropout(x, y, p, seed, offset=0, step=None, stream=None) -> None:
+    """y = x / keep where the element's random bits keep it, 0 elsewhere; the
+    mask is a function of (element, seed, offset + step) and never stored, so
+    the backward is the same call on the upstream gradient. y may be x."""
+    load()
+    dev, n = _current_device(x), x.numel()
+    code = _code(x.dtype)
+    if y.numel() != n:
+        raise ValueError(f"y holds {y.numel()} values, x {n}")
+    _check(_lib.rib_dropout(_arg("x", x, n, code, dev), _arg("y", y, n, code, dev), code, n, float(p), int(seed),
+                            int(offset), _step_arg(step, dev), _stream(stream)))
+
+
+def residual_norm_desc(T, C, x_dtype, dtype, pre="layer", post="none", eps=1e-5, rows_per_group=None, p=0.0, seed=0,
+                       offset=0) -> ResidualNormDesc:
+    """Descriptor of one join of a block with its residual stream: T rows of C
+    values, the stream in torch dtype x_dtype, the branch, gate and h in dtype;
+    pre and post are "none", "layer" or "rms"; rows_per_group rows share a row
+    of scale (all of them by default)."""
+    for n in (pre, post):
+        if n not in _NORMS:
+            raise ValueError(f"norm {n!r}: one of {sorted(_NORMS)}")
+    return ResidualNormDesc(T, C, max(1, T) if rows_per_group is None else rows_per_group, _code(x_dtype), _code(dtype),
+                            _NORMS[pre], _NORMS[post], float(eps), float(p), int(seed), int(offset))
+
+
+def _norm_groups(d: ResidualNormDesc) -> int:
+    return -(-d.T // d.rows_per_group) if d.rows_per_group > 0 else 0
+
+
+def rib_residual_norm(desc: ResidualNormDesc, x, y=None, gate=None, scale=None, post_w=None, post_b=None, pre_w=None,
+                      pre_b=None, x_out=None, h=None, step=None, stream=None) -> None:
+    """x_out = x + dropout(scale * gate * (N_post(y) post_w + post_b)) and
+    h = N_pre(x_out) pre_w + pre_b (see include/rib.h)."""
+    load()
+    dev, d = _current_device(x), desc
+    n, C, xc, c = d.T * d.C, d.C, d.x_dtype, d.dtype
+    _check(_lib.rib_residual_norm(
+        ctypes.byref(d), _arg("x", x, n, xc, dev), _arg("y", y, n, c, dev), _arg("gate", gate, n, c, dev),
+        _arg("scale", scale, _norm_groups(d) * C, RIB_F32, dev), _arg("post_w", post_w, C, RIB_F32, dev),
+        _arg("post_b", post_b, C, RIB_F32, dev), _arg("pre_w", pre_w, C, RIB_F32, dev), _arg("pre_b", pre_b, C, RIB_F32, dev),
+        _arg("x_out", x_out, n, xc, dev), _arg("h", h, n, c, dev), _step_arg(step, dev), _stream(stream)))
+
+
+def rib_residual_norm_bwd_workspace_size(desc: ResidualNormDesc) -> int:
+    return load().rib_residual_norm_bwd_workspace_size(ctypes.byref(desc))
+
+
+def rib_residual_norm_bwd(desc: ResidualNormDesc, x_out, y=None, gate=None, scale=None, post_w=None, post_b=None,
+                          pre_w=None, dx_out=None, dh=None, dx=None, dy=None, dgate=None, dscale=None, dpost_w=None,
+                          dpost_b=None, dpre_w=None, dpre_b=None, workspace=None, step=None, stream=None) -> None:
+    """Gradients of rib_residual_norm from dx_out (the stream's, may be None)
+    and dh; each output may be None (see include/rib.h)."""
+    load()
+    d = desc
+    dev = _current_device(x_out if x_out is not None else dx_out)
+    n, C, xc, c, g = d.T * d.C, d.C, d.x_dtype, d.dtype, _norm_groups(d) * d.C
+    if workspace is not None and (not workspace.is_cuda or workspace.device.index != dev or not workspace.is_contiguous()):
+        raise ValueError("workspace is a contiguous tensor of the current device")
+    _check(_lib.rib_residual_norm_bwd(
+        ctypes.byref(d), _arg("x_out", x_out, n, xc, dev), _arg("y", y, n, c, dev), _arg("gate", gate, n, c, dev),
+        _arg("scale", scale, g, RIB_F32, dev), _arg("post_w", post_w, C, RIB_F32, dev), _arg("post_b", post_b, C, RIB_F32, dev),
+        _arg("pre_w", pre_w, C, RIB_F32, dev), _arg("dx_out", dx_out, n, xc, dev), _arg("dh", dh, n, c, dev),
+        _arg("dx", dx, n, xc, dev), _arg("dy", dy, n, c, dev), _arg("dgate", dgate, n, c, dev),
+        _arg("dscale", dscale, g, RIB_F32, dev), _arg("dpost_w", dpost_w, C, RIB_F32, dev),
+        _arg("dpost_b", dpost_b, C, RIB_F32, dev), _arg("dpre_w", dpre_w, C, RIB_F32, dev),
+        _arg("dpre_b", dpre_b, C, RIB_F32, dev), None if workspace is None else workspace.data_ptr(),
+        0 if workspace is None else workspace.numel() * workspace.element_size(), _step_arg(step, dev), _stream(stream)))
