@@ -489,6 +489,58 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* desc, const void*
                                  float* dpost_w, float* dpost_b, float* dpre_w, float* dpre_b, void* workspace,
                                  size_t workspace_bytes, const uint64_t* step, cudaStream_t stream);
 
+/* Differential attention: per sequence and query head h, with its key head,
+ *   O = (softmax(scale Q1 K1^T) - lam[h] softmax(scale Q2 K2^T)) V
+ * Tensors are [batch][tokens][heads][width] with the widths contiguous.
+ * Query heads h * (q_heads / kv_heads) .. share key head h. A sequence is a
+ * batch item, or with window > 0 one window x window cell of each item's map
+ * [height][width] (q_len = k_len = height * width, cells at the right and
+ * lower edge are cut off there). */
+typedef struct {
+  int batch, q_len, k_len;
+  int q_heads, kv_heads;    /* q_heads a multiple of kv_heads */
+  int d, dv;                /* widths of queries and keys (<= 64) and of values
+                               (<= 128), multiples of 8 */
+  rib_dtype dtype;          /* of every tensor but lam: RIB_BF16 or RIB_F16 */
+  rib_dtype lam_dtype;      /* of lam and dlam: RIB_F32 or dtype */
+  float scale;              /* > 0 */
+  int causal;               /* query t sees the keys up to t + keys - q_len */
+  int window, width;        /* both 0: sequences; window <= 1024 */
+  /* elements between batch items, tokens and heads; three zeros: contiguous.
+   * Multiples of 8. q: q1, q2 and their gradients, k: k1, k2, v: v, o: o, o2
+   * and dO. What is written may not overlap. */
+  long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];
+} rib_diff_attn_desc;
+
+/* Forward. lam [q_heads]. k_lens: int32 [batch], keys of each item (clamped to
+ * 0..k_len), or NULL for k_len each; keys behind the length are never read,
+ * and a row that sees no key gets o = 0 and lse = -inf. For the backward: o2
+ * (the second map's output, layout of o) and lse fp32 [2][batch][q_heads]
+ * [q_len] (natural logarithm, both maps); else NULL. Scores, softmax sums and
+ * both maps' outputs are fp32; the probabilities take dtype for the product
+ * with V. fp16 results saturate at +-65504. Few query rows over long keys run
+ * as parts that a second kernel joins: workspace >=
+ * rib_diff_attention_workspace_size() bytes (0 otherwise; NULL then). Tensors
+ * and workspace 16-byte aligned. A row whose scores hold a NaN or an infinity
+ * becomes NaN. */
+size_t rib_diff_attention_workspace_size(const rib_diff_attn_desc* desc);
+rib_status rib_diff_attention(const rib_diff_attn_desc* desc, const void* q1, const void* q2, const void* k1, const void* k2,
+                              const void* v, const void* lam, const int* k_lens, void* o, void* o2, float* lse,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Backward from dO (layout of o) and the forward's o, o2 and lse: all
+ * gradients, overwritten, in the layouts of their tensors; those of keys
+ * behind a length are 0, those of a shared key head sums over its query heads.
+ * Probabilities and score gradients take dtype for the products (fp16 ones are
+ * held times 64: an |P (dP - D)| above 1023 becomes infinite, which loss
+ * scaling looks for). Deterministic: the same bits on every run. workspace >=
+ * rib_diff_attention_bwd_workspace_size() bytes, 16-byte aligned. */
+size_t rib_diff_attention_bwd_workspace_size(const rib_diff_attn_desc* desc);
+rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* desc, const void* q1, const void* q2, const void* k1, const void* k2,
+                                  const void* v, const void* lam, const int* k_lens, const void* o, const void* o2,
+                                  const float* lse, const void* dO, void* dq1, void* dq2, void* dk1, void* dk2, void* dv,
+                                  void* dlam, void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -113,3 +113,88 @@ def test_binding_refusals():
         rib.residual_norm_desc(4, 48, torch.float64, torch.bfloat16)
     with pytest.raises(ValueError):
         rib.residual_norm_desc(4, 48, torch.float32, torch.bfloat16, pre="batch")
+
+
+# ------------------------------------------------------ differential attention
+def _attn(**kw):
+    a = dict(batch=2, q_len=70, k_len=90, q_heads=4, kv_heads=2, d=16, dv=32, scale=0.25, dtype=torch.bfloat16)
+    after = {k: kw.pop(k) for k in list(kw) if k in ("dtype_code", "lam_code")}
+    a.update(kw)
+    d = rib.diff_attn_desc(**a)
+    if "dtype_code" in after:
+        d.dtype = after["dtype_code"]
+    if "lam_code" in after:
+        d.lam_dtype = after["lam_code"]
+    return ctypes.byref(d)
+
+
+ATTN = [P] * 5 + [P, None, P, P, P, P, 1 << 30, None]               # q1, q2, k1, k2, v, lam, k_lens, o, o2, lse, ws, bytes, stream
+ATTN_BWD = [P] * 5 + [P, None] + [P] * 10 + [P, 1 << 30, None]      # ..., o, o2, lse, dO, dq1, dq2, dk1, dk2, dv, dlam, ws, bytes, stream
+
+
+@pytest.mark.parametrize("kw,st", [
+    ({"batch": -1}, INVALID), ({"q_len": -1}, INVALID), ({"k_len": -1}, INVALID), ({"q_heads": 0}, INVALID), ({"kv_heads": 0}, INVALID),
+    ({"kv_heads": 3}, INVALID), ({"d": 0}, INVALID), ({"dv": -8}, INVALID), ({"d": 12}, UNSUPPORTED), ({"d": 72}, UNSUPPORTED),
+    ({"dv": 136}, UNSUPPORTED), ({"scale": 0.0}, INVALID), ({"scale": -1.0}, INVALID), ({"scale": float("nan")}, INVALID),
+    ({"scale": float("inf")}, INVALID), ({"dtype_code": 1}, INVALID), ({"dtype_code": 7}, INVALID), ({"lam_code": 2}, INVALID),
+    ({"window": 8}, INVALID), ({"width": 8}, INVALID), ({"window": -1, "width": 8}, INVALID), ({"window": 8, "width": 10}, INVALID),
+    ({"window": 8, "width": 8, "k_len": 70}, INVALID), ({"window": 8, "width": 10, "k_len": 70, "causal": True}, INVALID),
+    ({"window": 1025, "width": 10, "k_len": 70}, UNSUPPORTED), ({"q_len": 1 << 30, "kv_heads": 1}, UNSUPPORTED),
+    ({"batch": 1 << 30}, UNSUPPORTED), ({"k_len": 0x7FFFFFFF}, UNSUPPORTED),
+    ({"q_stride": (4480, 64, 4)}, ALIGNMENT), ({"k_stride": (-8, 32, 16)}, ALIGNMENT), ({"o_stride": (0, 128, 32)}, INVALID),
+    ({"o_stride": (8960, 32, 32)}, INVALID),
+], ids=str)
+def test_diff_attention_descriptor_refusals(lib, kw, st):
+    d = _attn(**kw)
+    assert lib.rib_diff_attention(d, *ATTN) == st
+    assert lib.rib_diff_attention_bwd(d, *ATTN_BWD) == st
+    assert lib.rib_diff_attention_workspace_size(d) == 0
+    assert lib.rib_diff_attention_bwd_workspace_size(d) == 0
+
+
+def test_diff_attention_argument_refusals(lib):
+    f = lambda d, a: lib.rib_diff_attention(d, *a)  # noqa: E731
+    b = lambda d, a: lib.rib_diff_attention_bwd(d, *a)  # noqa: E731
+    assert f(None, ATTN) == INVALID and b(None, ATTN_BWD) == INVALID
+    for i in (0, 1, 2, 3, 4, 5, 7):
+        assert f(_attn(), _with(ATTN, **{f"_{i}": None})) == INVALID, i
+    for i in [0, 1, 2, 3, 4, 5] + list(range(7, 18)):
+        assert b(_attn(), _with(ATTN_BWD, **{f"_{i}": None})) == INVALID, i
+    for i in (0, 1, 2, 3, 4, 7, 8, 10):
+        assert f(_attn(), _with(ATTN, **{f"_{i}": 264})) == ALIGNMENT, i
+    for i in [0, 1, 2, 3, 4, 7, 8] + list(range(10, 16)) + [17]:
+        assert b(_attn(), _with(ATTN_BWD, **{f"_{i}": 264})) == ALIGNMENT, i
+    assert f(_attn(), _with(ATTN, _5=257)) == ALIGNMENT and f(_attn(), _with(ATTN, _6=258)) == ALIGNMENT
+    assert f(_attn(lam_dtype=torch.float32), _with(ATTN, _5=258)) == ALIGNMENT
+    assert b(_attn(), _with(ATTN_BWD, _9=258)) == ALIGNMENT and b(_attn(), _with(ATTN_BWD, _16=257)) == ALIGNMENT
+    w = dict(window=8, width=10, k_len=70)
+    assert f(_attn(**w), _with(ATTN, _6=P)) == INVALID and b(_attn(**w), _with(ATTN_BWD, _6=P)) == INVALID   # windows and lengths
+    assert b(_attn(), _with(ATTN_BWD, _18=100)) == INVALID                                                   # workspace too small
+    # gradients that would lie on one another; a broadcast input is fine in the forward
+    for k in ("q_stride", "k_stride"):
+        assert b(_attn(**{k: (0, 64, 16)}), ATTN_BWD) == INVALID
+    assert b(_attn(v_stride=(0, 64, 32)), ATTN_BWD) == INVALID
+    long = dict(batch=1, q_len=1, k_len=100000)
+    assert lib.rib_diff_attention_workspace_size(_attn(**long)) > 0
+    assert f(_attn(**long), _with(ATTN, _10=None)) == INVALID and f(_attn(**long), _with(ATTN, _11=64)) == INVALID
+    assert f(_attn(batch=0), [None] * 11 + [0, None]) == 0 and f(_attn(q_len=0), [None] * 11 + [0, None]) == 0
+
+
+def test_diff_attention_workspace_sizes(lib):
+    # six arrays of 32-bit row constants, rows of a key head padded to 128
+    assert rib.rib_diff_attention_bwd_workspace_size(_attn()._obj) == 2 * 2 * 256 * 6 * 4
+    assert rib.rib_diff_attention_bwd_workspace_size(_attn(q_len=70, k_len=70, window=8, width=10)._obj) == 2 * 2 * 2 * 128 * 6 * 4
+    assert rib.rib_diff_attention_workspace_size(_attn()._obj) == 0
+    for kw in ({"batch": 0}, {"q_len": 0}, {"k_len": 0}):
+        assert rib.rib_diff_attention_workspace_size(_attn(**kw)._obj) == 0
+
+
+def test_diff_attention_binding_refusals():
+    d = rib.diff_attn_desc(1, 4, 4, 2, 2, 16, 32, 0.25, torch.bfloat16)
+    t = torch.zeros(1, 4, 2, 16, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        rib.rib_diff_attention(d, t, t, t, t, t, t, o=t)          # host tensors
+    with pytest.raises(ValueError):
+        rib.diff_attn_desc(1, 4, 4, 2, 2, 16, 32, 0.25, torch.int32)
+    with pytest.raises(ValueError):
+        _lib._strided_arg("q1", t, 4, 2, 16, d.q_stride, d, 0)

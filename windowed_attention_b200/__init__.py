@@ -15,6 +15,8 @@ from ._lib import (  # noqa: F401
     rib_conv_ffn, rib_conv_ffn_workspace_size,
     ResidualNormDesc, residual_norm_desc, rib_dropout, rib_residual_norm, rib_residual_norm_bwd,
     rib_residual_norm_bwd_workspace_size,
+    DiffAttnDesc, diff_attn_desc, rib_diff_attention, rib_diff_attention_workspace_size, rib_diff_attention_bwd,
+    rib_diff_attention_bwd_workspace_size,
 )
 from .workloads import WORKLOADS, LayerShape, Workload, make_inputs  # noqa: F401
 

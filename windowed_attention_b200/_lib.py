@@ -62,6 +62,12 @@ class ResidualNormDesc(ctypes.Structure):
                 ("eps", ctypes.c_float), ("p", ctypes.c_float), ("seed", ctypes.c_uint64), ("offset", ctypes.c_uint64)]
 
 
+class DiffAttnDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("batch", "q_len", "k_len", "q_heads", "kv_heads", "d", "dv", "dtype", "lam_dtype")] + \
+        [("scale", ctypes.c_float)] + [(n, ctypes.c_int) for n in ("causal", "window", "width")] + \
+        [(n, ctypes.c_longlong * 3) for n in ("q_stride", "k_stride", "v_stride", "o_stride")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 _vp, _i, _f, _sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
 
@@ -98,6 +104,10 @@ _SIGNATURES = {
     "rib_residual_norm": ([ctypes.POINTER(ResidualNormDesc)] + [_vp] * 12, _i),
     "rib_residual_norm_bwd_workspace_size": ([ctypes.POINTER(ResidualNormDesc)], _sz),
     "rib_residual_norm_bwd": ([ctypes.POINTER(ResidualNormDesc)] + [_vp] * 18 + [_sz, _vp, _vp], _i),
+    "rib_diff_attention_workspace_size": ([ctypes.POINTER(DiffAttnDesc)], _sz),
+    "rib_diff_attention": ([ctypes.POINTER(DiffAttnDesc)] + [_vp] * 11 + [_sz, _vp], _i),
+    "rib_diff_attention_bwd_workspace_size": ([ctypes.POINTER(DiffAttnDesc)], _sz),
+    "rib_diff_attention_bwd": ([ctypes.POINTER(DiffAttnDesc)] + [_vp] * 18 + [_sz, _vp], _i),
 }
 
 
@@ -493,3 +503,94 @@ def rib_residual_norm_bwd(desc: ResidualNormDesc, x_out, y=None, gate=None, scal
         _arg("dpost_b", dpost_b, C, RIB_F32, dev), _arg("dpre_w", dpre_w, C, RIB_F32, dev),
         _arg("dpre_b", dpre_b, C, RIB_F32, dev), None if workspace is None else workspace.data_ptr(),
         0 if workspace is None else workspace.numel() * workspace.element_size(), _step_arg(step, dev), _stream(stream)))
+
+
+def diff_attn_desc(batch, q_len, k_len, q_heads, kv_heads, d, dv, scale, dtype, lam_dtype=None, causal=False, window=0, width=0,
+                   q_stride=None, k_stride=None, v_stride=None, o_stride=None) -> DiffAttnDesc:
+    """Descriptor of a differential attention: tensors [batch, tokens, heads,
+    width] in torch dtype `dtype` (bfloat16 or float16), lam in lam_dtype
+    (`dtype` by default, or float32). window and width: over the window x
+    window cells of a map `width` wide instead of whole sequences. The strides
+    are elements between batch items, tokens and heads (None: contiguous)."""
+    s = [(ctypes.c_longlong * 3)(*(x or (0, 0, 0))) for x in (q_stride, k_stride, v_stride, o_stride)]
+    return DiffAttnDesc(batch, q_len, k_len, q_heads, kv_heads, d, dv, _code(dtype), _code(dtype if lam_dtype is None else lam_dtype),
+                        float(scale), int(bool(causal)), window, width, *s)
+
+
+def _strided_arg(name, t, tokens, heads, width, strides, desc, device) -> Optional[int]:
+    """Pointer of a device tensor [batch, tokens, heads, width] laid out as the descriptor says."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.device.index != device:
+        raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
+    if _TORCH_CODE.get(t.dtype) != desc.dtype:
+        raise ValueError(f"{name} is {t.dtype}")
+    shape = (desc.batch, tokens, heads, width)
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} is {tuple(t.shape)}, the descriptor says {shape}")
+    if any(strides):
+        want = (*strides, 1)
+        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
+            raise ValueError(f"{name} has strides {t.stride()}, the descriptor says {want}")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: not contiguous, and the descriptor names no strides")
+    return t.data_ptr()
+
+
+def _workspace_arg(ws, device):
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or ws.device.index != device or not ws.is_contiguous():
+        raise ValueError("workspace is a contiguous tensor of the current device")
+    n = ws.numel() * ws.element_size()
+    return (ws.data_ptr() if n else None), n
+
+
+def _diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev):
+    import torch
+    if k_lens is not None and (k_lens.dtype != torch.int32 or k_lens.numel() < d.batch or not k_lens.is_cuda or
+                               k_lens.device.index != dev or not k_lens.is_contiguous()):
+        raise ValueError("k_lens holds one int32 a batch item on the current device")
+    return (_strided_arg("q1", q1, d.q_len, d.q_heads, d.d, d.q_stride, d, dev),
+            _strided_arg("q2", q2, d.q_len, d.q_heads, d.d, d.q_stride, d, dev),
+            _strided_arg("k1", k1, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev),
+            _strided_arg("k2", k2, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev),
+            _strided_arg("v", v, d.k_len, d.kv_heads, d.dv, d.v_stride, d, dev),
+            _arg("lam", lam, d.q_heads, d.lam_dtype, dev), None if k_lens is None else k_lens.data_ptr())
+
+
+def rib_diff_attention_workspace_size(desc: DiffAttnDesc) -> int:
+    return load().rib_diff_attention_workspace_size(ctypes.byref(desc))
+
+
+def rib_diff_attention(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens=None, o=None, o2=None, lse=None, workspace=None,
+                       stream=None) -> None:
+    """o = (softmax(scale q1 k1^T) - lam softmax(scale q2 k2^T)) v; o2 and lse
+    (None for inference) are what the backward needs (see include/rib.h)."""
+    load()
+    dev, d = _current_device(q1), desc
+    _check(_lib.rib_diff_attention(
+        ctypes.byref(d), *_diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev),
+        _strided_arg("o", o, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev),
+        _strided_arg("o2", o2, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev),
+        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), *_workspace_arg(workspace, dev), _stream(stream)))
+
+
+def rib_diff_attention_bwd_workspace_size(desc: DiffAttnDesc) -> int:
+    return load().rib_diff_attention_bwd_workspace_size(ctypes.byref(desc))
+
+
+def rib_diff_attention_bwd(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens, o, o2, lse, do, dq1, dq2, dk1, dk2, dv, dlam,
+                           workspace, stream=None) -> None:
+    """Every gradient of rib_diff_attention from do and the forward's o, o2 and
+    lse (see include/rib.h)."""
+    load()
+    dev, d = _current_device(q1), desc
+    out = [_strided_arg(n, t, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev) for n, t in (("o", o), ("o2", o2), ("do", do))]
+    dq = [_strided_arg(n, t, d.q_len, d.q_heads, d.d, d.q_stride, d, dev) for n, t in (("dq1", dq1), ("dq2", dq2))]
+    dk = [_strided_arg(n, t, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev) for n, t in (("dk1", dk1), ("dk2", dk2))]
+    _check(_lib.rib_diff_attention_bwd(
+        ctypes.byref(d), *_diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev), out[0], out[1],
+        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), out[2], *dq, *dk,
+        _strided_arg("dv", dv, d.k_len, d.kv_heads, d.dv, d.v_stride, d, dev), _arg("dlam", dlam, d.q_heads, d.lam_dtype, dev),
+        *_workspace_arg(workspace, dev), _stream(stream)))

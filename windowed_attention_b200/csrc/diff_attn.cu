@@ -1,0 +1,180 @@
+// Entry points of differential attention: argument checks, the geometry that
+// the kernels read, workspace sizes.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <cstdio>
+
+#include "diff_attn.cuh"
+
+namespace rib {
+namespace {
+
+rib_status bad(const char* who, rib_status st, const char* what) {
+  char buf[200];
+  std::snprintf(buf, sizeof(buf), "%s: %s", who, what);
+  return fail(st, buf);
+}
+
+// The strides of a tensor [batch][tokens][heads][e]; all zero means contiguous.
+DiffStrides strides(const long long (&s)[3], long long tokens, int heads, int e) {
+  if (!s[0] && !s[1] && !s[2]) return {tokens * heads * e, static_cast<long long>(heads) * e, e};
+  return {s[0], s[1], s[2]};
+}
+bool bad_strides(const DiffStrides& s) { return s.b < 0 || s.t < 0 || s.h < 0 || s.b % 8 || s.t % 8 || s.h % 8; }
+// Written tensors may not lay two values on one place: the head stride holds a
+// row of e, the token stride a token's heads and the batch stride an item.
+bool overlaps(const DiffStrides& s, int batch, long long tokens, int heads, int e) {
+  if (batch == 0 || tokens == 0) return false;
+  struct Axis { long long n, st; } ax[3] = {{heads, s.h}, {tokens, s.t}, {batch, s.b}};
+  for (int i = 0; i < 3; ++i)
+    for (int j = i + 1; j < 3; ++j)
+      if (ax[j].st < ax[i].st) { const Axis x = ax[i]; ax[i] = ax[j]; ax[j] = x; }
+  long long reach = e;   // values from the first to behind the last of the axes so far
+  for (const Axis& x : ax) {
+    if (x.n <= 1) continue;
+    if (x.st < reach) return true;
+    reach += (x.n - 1) * x.st;
+  }
+  return false;
+}
+
+rib_status geometry(const char* who, const rib_diff_attn_desc* d, DiffGeom* g) {
+  if (!d) return bad(who, RIB_ERR_INVALID_ARG, "null descriptor");
+  if (d->batch < 0 || d->q_len < 0 || d->k_len < 0 || d->q_heads <= 0 || d->kv_heads <= 0 || d->d <= 0 || d->dv <= 0)
+    return bad(who, RIB_ERR_INVALID_ARG, "sizes: batch and lengths >= 0, heads and widths positive");
+  if (d->q_heads % d->kv_heads) return bad(who, RIB_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return bad(who, RIB_ERR_INVALID_ARG, "scale must be positive and finite");
+  if (d->dtype != RIB_BF16 && d->dtype != RIB_F16) return bad(who, RIB_ERR_INVALID_ARG, "dtype must be RIB_BF16 or RIB_F16");
+  if (d->lam_dtype != RIB_F32 && d->lam_dtype != d->dtype)
+    return bad(who, RIB_ERR_INVALID_ARG, "lam_dtype must be RIB_F32 or dtype");
+  if (d->d % 8 || d->dv % 8 || d->d > 64 || d->dv > 128) return bad(who, RIB_ERR_UNSUPPORTED, "needs d <= 64 and dv <= 128, multiples of 8");
+  if (d->window < 0 || d->width < 0 || (d->window > 0) != (d->width > 0))
+    return bad(who, RIB_ERR_INVALID_ARG, "window and width go together");
+  if (d->window > 0) {
+    if (d->q_len != d->k_len || d->q_len % d->width) return bad(who, RIB_ERR_INVALID_ARG, "a map has q_len = k_len = height * width");
+    if (d->causal) return bad(who, RIB_ERR_INVALID_ARG, "windows have no causal mask");
+    if (d->window > 1024) return bad(who, RIB_ERR_UNSUPPORTED, "window above 1024");
+  }
+  *g = DiffGeom{};
+  g->batch = d->batch; g->q_len = d->q_len; g->k_len = d->k_len; g->q_heads = d->q_heads; g->kv_heads = d->kv_heads;
+  g->group = d->q_heads / d->kv_heads;
+  g->d = d->d; g->dv = d->dv;
+  g->window = d->window; g->width = d->width; g->causal = d->causal != 0; g->lam_f32 = d->lam_dtype == RIB_F32;
+  if (d->window > 0) {
+    g->height = d->q_len / d->width;
+    g->nwx = (d->width - 1) / d->window + 1;
+    g->nwy = g->height > 0 ? (g->height - 1) / d->window + 1 : 0;
+  }
+  g->group_magic = div_magic(static_cast<uint32_t>(g->group));
+  g->scale = d->scale;
+  g->scale_log2 = d->scale * kDiffLog2e;
+  g->q = strides(d->q_stride, d->q_len, d->q_heads, d->d);
+  g->k = strides(d->k_stride, d->k_len, d->kv_heads, d->d);
+  g->v = strides(d->v_stride, d->k_len, d->kv_heads, d->dv);
+  g->o = strides(d->o_stride, d->q_len, d->q_heads, d->dv);
+  // rows are ints (with a tile behind the last), and row / group is exact below 2^32
+  const long long rows = static_cast<long long>(d->q_len) * g->group;
+  if (rows > 0x7FFFFFFFll - 256 || rows > 0xFFFFFFFFll / g->group - 256 || d->k_len > 0x7FFFFFFF - 256 || d->q_len > 0x7FFFFFFF - 256)
+    return bad(who, RIB_ERR_UNSUPPORTED, "sequences too long");
+  // units of work are ints: (sequences, key heads, tiles, splits)
+  const long long seqs = static_cast<long long>(d->batch) * (d->window ? static_cast<long long>(g->nwx) * g->nwy : 1);
+  const long long tiles = (diff_max_rows(*g) > diff_max_keys(*g) ? diff_max_rows(*g) : diff_max_keys(*g)) / 32 + 1;
+  if (seqs > 0x7FFFFFFFll / d->kv_heads || seqs * d->kv_heads > 0x3FFFFFFFll / (tiles > 64 ? tiles : 64))
+    return bad(who, RIB_ERR_UNSUPPORTED, "too many sequences and heads");
+  if (bad_strides(g->q) || bad_strides(g->k) || bad_strides(g->v) || bad_strides(g->o))
+    return bad(who, RIB_ERR_ALIGNMENT, "strides must be non-negative multiples of 8 elements");
+  if (overlaps(g->o, d->batch, d->q_len, d->q_heads, d->dv)) return bad(who, RIB_ERR_INVALID_ARG, "o_stride lays values of o on one another");
+  return RIB_OK;
+}
+
+bool misaligned(std::initializer_list<const void*> ps, uintptr_t to) {
+  for (const void* p : ps)
+    if (reinterpret_cast<uintptr_t>(p) % to) return true;
+  return false;
+}
+
+uintptr_t lam_size(const rib_diff_attn_desc* d) { return d->lam_dtype == RIB_F32 ? 4 : 2; }
+
+long long row_values(const DiffGeom& g) { return static_cast<long long>(diff_sequences(g)) * g.kv_heads * diff_rows_pad(g); }
+
+}  // namespace
+}  // namespace rib
+
+using namespace rib;
+
+extern "C" {
+
+size_t rib_diff_attention_workspace_size(const rib_diff_attn_desc* d) {
+  DiffGeom g;
+  return geometry("rib_diff_attention_workspace_size", d, &g) == RIB_OK ? diff_split_bytes(g) : 0;
+}
+
+rib_status rib_diff_attention(const rib_diff_attn_desc* d, const void* q1, const void* q2, const void* k1, const void* k2, const void* v,
+                              const void* lam, const int* k_lens, void* o, void* o2, float* lse, void* ws, size_t ws_bytes,
+                              cudaStream_t stream) {
+  const char* who = "rib_diff_attention";
+  DiffFwdArgs a{};
+  rib_status st = geometry(who, d, &a.g);
+  if (st != RIB_OK) return st;
+  if (d->batch == 0 || d->q_len == 0) return RIB_OK;   // no rows: nothing is written
+  const bool keys = d->k_len > 0;                      // empty tensors may have null pointers
+  if (!q1 || !q2 || !lam || !o || (keys && (!k1 || !k2 || !v))) return bad(who, RIB_ERR_INVALID_ARG, "null pointer");
+  if (k_lens && d->window) return bad(who, RIB_ERR_INVALID_ARG, "windows have no key lengths");
+  if (misaligned({q1, q2, k1, k2, v, o, o2, ws}, 16) || misaligned({lse, k_lens}, 4) || misaligned({lam}, lam_size(d)))
+    return bad(who, RIB_ERR_ALIGNMENT, "tensors and workspace need 16 bytes, lam, lse and k_lens their element's");
+  a.splits = diff_splits(a.g);
+  if (a.splits > 1) {
+    if (!ws || ws_bytes < diff_split_bytes(a.g)) return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
+    a.part = static_cast<float*>(ws);
+  }
+  a.g.k_lens = k_lens;
+  a.q1 = q1; a.q2 = q2; a.k1 = k1; a.k2 = k2; a.v = v; a.lam = lam;
+  a.o = o; a.o2 = o2; a.lse = lse;
+  if (!(a.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
+  const cudaError_t e = launch_diff_attn_fwd(a, d->dtype == RIB_F16, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rib_diff_attention launch");
+  return RIB_OK;
+}
+
+size_t rib_diff_attention_bwd_workspace_size(const rib_diff_attn_desc* d) {
+  DiffGeom g;
+  return geometry("rib_diff_attention_bwd_workspace_size", d, &g) == RIB_OK ? row_values(g) * kRowArrays * sizeof(float) : 0;
+}
+
+rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, const void* q2, const void* k1, const void* k2, const void* v,
+                                  const void* lam, const int* k_lens, const void* o, const void* o2, const float* lse, const void* dO,
+                                  void* dq1, void* dq2, void* dk1, void* dk2, void* dv, void* dlam, void* ws, size_t ws_bytes,
+                                  cudaStream_t stream) {
+  const char* who = "rib_diff_attention_bwd";
+  DiffBwdArgs a{};
+  rib_status st = geometry(who, d, &a.g);
+  if (st != RIB_OK) return st;
+  const DiffGeom& g = a.g;
+  const bool rows = d->batch > 0 && d->q_len > 0, keys = d->batch > 0 && d->k_len > 0;
+  if (!lam || !dlam || (rows && (!q1 || !q2 || !o || !o2 || !lse || !dO || !dq1 || !dq2)) ||
+      (keys && (!k1 || !k2 || !v || !dk1 || !dk2 || !dv)))
+    return bad(who, RIB_ERR_INVALID_ARG, "null pointer");
+  if (k_lens && d->window) return bad(who, RIB_ERR_INVALID_ARG, "windows have no key lengths");
+  if (misaligned({q1, q2, k1, k2, v, o, o2, dO, dq1, dq2, dk1, dk2, dv, ws}, 16) || misaligned({lse, k_lens}, 4) ||
+      misaligned({lam, dlam}, lam_size(d)))
+    return bad(who, RIB_ERR_ALIGNMENT, "tensors and workspace need 16 bytes, lam, dlam, lse and k_lens their element's");
+  if (overlaps(g.q, d->batch, d->q_len, d->q_heads, d->d) || overlaps(g.k, d->batch, d->k_len, d->kv_heads, d->d) ||
+      overlaps(g.v, d->batch, d->k_len, d->kv_heads, d->dv))
+    return bad(who, RIB_ERR_INVALID_ARG, "strides lay gradients on one another");
+  a.rows_pad = static_cast<int>(diff_rows_pad(g));
+  a.row_stride = row_values(g);
+  if (rows && (!ws || ws_bytes < a.row_stride * kRowArrays * sizeof(float)))
+    return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
+  a.rows = static_cast<float*>(ws);
+  a.g.k_lens = k_lens;
+  a.q1 = q1; a.q2 = q2; a.k1 = k1; a.k2 = k2; a.v = v; a.lam = lam; a.o = o; a.o2 = o2; a.lse = lse; a.dO = dO;
+  a.dq1 = dq1; a.dq2 = dq2; a.dk1 = dk1; a.dk2 = dk2; a.dv = dv; a.dlam = dlam;
+  if (!(a.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
+  const cudaError_t e = launch_diff_attn_bwd(a, d->dtype == RIB_F16, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "rib_diff_attention_bwd launch");
+  return RIB_OK;
+}
+
+}  // extern "C"

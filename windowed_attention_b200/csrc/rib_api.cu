@@ -74,6 +74,21 @@ const char* site_name(int s) {
     case 307: return "attention backward: accumulate MMAs";
     case 308: return "attention backward: final MMA drain";
     case 309: return "attention backward: TMA drain";
+    case 401: return "differential attention: queries loaded";
+    case 402: return "differential attention: stage loaded";
+    case 403: return "differential attention: free stage";
+    case 404: return "differential attention: S ready";
+    case 405: return "differential attention: P written";
+    case 406: return "differential attention: P V";
+    case 407: return "differential attention: MMA drain";
+    case 421: return "differential attention backward: own tiles";
+    case 422: return "differential attention backward: stage loaded";
+    case 423: return "differential attention backward: free stage";
+    case 424: return "differential attention backward: S ready";
+    case 425: return "differential attention backward: S read";
+    case 426: return "differential attention backward: dS written";
+    case 427: return "differential attention backward: accumulate MMAs";
+    case 428: return "differential attention backward: MMA drain";
     case 901: return "self-test wait (nothing arrives)";
     default: return "unknown";
   }
