@@ -117,46 +117,89 @@ struct DiffTile {
   }
 };
 
-// 16 bytes into shared memory, or 16 zero bytes (nothing is read then).
-__device__ __forceinline__ void cp_async_16_or_zero(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
+// One row of a tensor into a tile, by a pair of lanes (par = 0, 1: they share
+// 32-byte sectors): two instructions a 16-byte piece, since the swizzle is an
+// exclusive or of the row's place. `size` is 16, or 0 for a row of zeros (src is
+// not read then). Pieces at or behind n (the tensor's width) are left as they are.
+template <int ROWS, int D>
+__device__ __forceinline__ void diff_load_row(uint32_t tile, int row, int par, const uint16_t* src, int size, int n) {
+  using T = DiffTile<ROWS, D>;
+  constexpr int per = T::COLS / 8;
+  const uint32_t dst = tile + T::offset(row, par);
+  const uint16_t* from = src + par * 8;
+#pragma unroll
+  for (int k = 0; k < T::CHUNKS / 2; ++k)
+    if (2 * k + par < n)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                   ::"r"((dst ^ ((2 * k % per) << 4)) + 2 * k / per * T::ATOM), "l"(from + 16 * k), "r"(size) : "memory");
 }
 
-// Rows first .. first + ROWS - 1 of a key-side tensor (one row a token) into a
-// tile; rows at or behind n and columns at or behind d become zero, so what a
-// mask hides never reaches a product.
-template <int ROWS, int D, int THREADS>
-__device__ __forceinline__ void diff_load_keys(uint32_t tile, const uint16_t* base, long long stride, const DiffSeq& s, int first, int n,
-                                               int d, int tid) {
-  using T = DiffTile<ROWS, D>;
-  static_assert(THREADS % T::CHUNKS == 0, "a thread keeps its column");
-  const int ch = tid % T::CHUNKS;
-#pragma unroll 4
-  for (int row = tid / T::CHUNKS; row < ROWS; row += THREADS / T::CHUNKS) {
-    const int t = first + row;
-    const bool real = t < n && ch * 8 < d;
-    cp_async_16_or_zero(tile + T::offset(row, ch), real ? base + s.token(t) * stride + ch * 8 : base, real);
+// Rows first .. first + ROWS - 1 of the key side (a row a token): k1, k2 and v
+// into three tiles one behind the other. Rows at or behind n become zero, so
+// what a mask hides never reaches a product. Every row is a pair of lanes.
+template <int ROWS, int D, int DV, int THREADS>
+__device__ __forceinline__ void diff_load_keys(uint32_t tile, const uint16_t* k1, const uint16_t* k2, const uint16_t* v, const DiffGeom& g,
+                                               const DiffSeq& s, int first, int n, int tid) {
+  const int par = tid & 1, nd = g.d / 8, nv = g.dv / 8;
+#pragma unroll
+  for (int row = tid >> 1; row < ROWS; row += THREADS / 2) {
+    const int t = first + row, size = t < n ? 16 : 0;
+    const long long token = t < n ? s.token(t) : 0;
+    diff_load_row<ROWS, D>(tile, row, par, k1 + token * g.k.t, size, nd);
+    diff_load_row<ROWS, D>(tile + DiffTile<ROWS, D>::BYTES, row, par, k2 + token * g.k.t, size, nd);
+    diff_load_row<ROWS, DV>(tile + 2 * DiffTile<ROWS, D>::BYTES, row, par, v + token * g.v.t, size, nv);
   }
 }
 
-// The same for a query-side tensor.
-template <int ROWS, int D, int THREADS>
-__device__ __forceinline__ void diff_load_queries(uint32_t tile, const uint16_t* base, const DiffStrides& st, const DiffGeom& g,
-                                                  const DiffSeq& s, int first, int n, int d, int tid) {
-  using T = DiffTile<ROWS, D>;
-  static_assert(THREADS % T::CHUNKS == 0, "a thread keeps its column");
-  const int ch = tid % T::CHUNKS;
-#pragma unroll 4
-  for (int row = tid / T::CHUNKS; row < ROWS; row += THREADS / T::CHUNKS) {
-    const int r = first + row;
-    const bool real = r < n && ch * 8 < d;
-    const int t = diff_row_token(g, r), h = r - t * g.group;
-    cp_async_16_or_zero(tile + T::offset(row, ch), real ? base + s.token(t) * st.t + h * st.h + ch * 8 : base, real);
+// The same for the query side: q1, q2 and (dO not null) dO.
+template <int ROWS, int D, int DV, int THREADS>
+__device__ __forceinline__ void diff_load_queries(uint32_t tile, const uint16_t* q1, const uint16_t* q2, const uint16_t* dO, const DiffGeom& g,
+                                                  const DiffSeq& s, int first, int n, int tid) {
+  const int par = tid & 1, nd = g.d / 8, nv = g.dv / 8;
+#pragma unroll
+  for (int row = tid >> 1; row < ROWS; row += THREADS / 2) {
+    const int r = first + row, size = r < n ? 16 : 0;
+    const int t = r < n ? diff_row_token(g, r) : 0, h = r < n ? r - t * g.group : 0;
+    const long long token = s.token(t), at = token * g.q.t + h * g.q.h;
+    diff_load_row<ROWS, D>(tile, row, par, q1 + at, size, nd);
+    diff_load_row<ROWS, D>(tile + DiffTile<ROWS, D>::BYTES, row, par, q2 + at, size, nd);
+    if (dO) diff_load_row<ROWS, DV>(tile + 2 * DiffTile<ROWS, D>::BYTES, row, par, dO + token * g.o.t + h * g.o.h, size, nv);
   }
+}
+
+// Zeros for the columns behind the tensors' widths, which no load writes: the
+// loader warps clear their tiles once (barrier 2 is theirs).
+template <int D, int DV, int THREADS>
+__device__ __forceinline__ void diff_clear(uint8_t* tiles, int bytes, const DiffGeom& g, int tid) {
+  if (g.d == D && g.dv == DV) return;
+  for (int i = tid * 16; i < bytes; i += THREADS * 16) *reinterpret_cast<uint4*>(tiles + i) = make_uint4(0u, 0u, 0u, 0u);
+  asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
 }
 
 __host__ __device__ constexpr uint32_t diff_idesc(bool f16, int N, bool b_mn) {
   return f16 ? idesc_f16(128, N, false, b_mn) : idesc_bf16(128, N, false, b_mn);
+}
+
+// 2^x for a pair of x in [-inf, 127] on the FMA pipe, for the share of the
+// exponentials that relieves the MUFU (16 a cycle and SM): exp2_poly_x2 with a
+// polynomial of degree 4, fitted for relative error on [-1/2, 1/2] (2.8e-6,
+// against 1.0e-4 of the cubic): the log-sum-exp goes out in fp32. A NaN gives
+// 0; callers see it in the other elements of its row.
+__device__ __forceinline__ void diff_exp2_poly(float x0, float x1, float& y0, float& y1) {
+  constexpr float kRound = 12582912.0f;   // 1.5 * 2^23
+  const uint64_t x = f2_pack(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+  const uint64_t t = f2_add(x, f2_pack(kRound, kRound));
+  const uint64_t j = f2_add(t, f2_pack(-kRound, -kRound));
+  const uint64_t f = f2_fma(j, f2_pack(-1.f, -1.f), x);
+  uint64_t p = f2_fma(f2_pack(0.00958285201f, 0.00958285201f), f, f2_pack(0.0559064262f, 0.0559064262f));
+  p = f2_fma(p, f, f2_pack(0.240240991f, 0.240240991f));
+  p = f2_fma(p, f, f2_pack(0.693124175f, 0.693124175f));
+  p = f2_fma(p, f, f2_pack(1.f, 1.f));
+  float p0, p1, t0, t1;
+  f2_unpack(p, p0, p1);
+  f2_unpack(t, t0, t1);
+  y0 = __uint_as_float(__float_as_uint(p0) + (__float_as_uint(t0) << 23));
+  y1 = __uint_as_float(__float_as_uint(p1) + (__float_as_uint(t1) << 23));
 }
 
 // Two fp32 as a packed pair of the operand type.

@@ -192,6 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
     const uint16_t* v = static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h;
     int told = -1;   // -1: nothing handed over, 0: the own tiles, i + 1: key tile i
     auto tell = [&](int upto) {
+      if (upto <= told) return;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0)
@@ -199,9 +200,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
       told = upto;
     };
     if (n > 0) {
-      diff_load_queries<kOwn, D, kLoaders>(so, static_cast<const uint16_t*>(a.q1) + qb, g.q, g, s, row0, rows, g.d, tid);
-      diff_load_queries<kOwn, D, kLoaders>(so + TQ::BYTES, static_cast<const uint16_t*>(a.q2) + qb, g.q, g, s, row0, rows, g.d, tid);
-      diff_load_queries<kOwn, DV, kLoaders>(so + 2 * TQ::BYTES, static_cast<const uint16_t*>(a.dO) + ob, g.o, g, s, row0, rows, g.dv, tid);
+      diff_clear<D, DV, kLoaders>(smem, Lay::OFF_BAR, g, tid);
+      diff_load_queries<kOwn, D, DV, kLoaders>(so, static_cast<const uint16_t*>(a.q1) + qb, static_cast<const uint16_t*>(a.q2) + qb,
+                                               static_cast<const uint16_t*>(a.dO) + ob, g, s, row0, rows, tid);
       cp_async_commit();
     }
     for (int i = 0; i < n; ++i) {
@@ -215,9 +216,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
         }
       }
       const uint32_t b = sst + st * Lay::STAGE;
-      diff_load_keys<kStream, D, kLoaders>(b, k1, g.k.t, s, i * kStream, s.nk, g.d, tid);
-      diff_load_keys<kStream, D, kLoaders>(b + TK::BYTES, k2, g.k.t, s, i * kStream, s.nk, g.d, tid);
-      diff_load_keys<kStream, DV, kLoaders>(b + 2 * TK::BYTES, v, g.v.t, s, i * kStream, s.nk, g.dv, tid);
+      diff_load_keys<kStream, D, DV, kLoaders>(b, k1, k2, v, g, s, i * kStream, s.nk, tid);
       cp_async_commit();
       cp_async_wait<1>();
       tell(i);
@@ -477,6 +476,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
     const float* consts = a.rows + static_cast<long long>(unit) * a.rows_pad;
     int told = -1;
     auto tell = [&](int upto) {
+      if (upto <= told) return;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0)
@@ -484,10 +484,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
       told = upto;
     };
     if (n > 0) {
-      diff_load_keys<kOwn, D, kLoaders>(so, static_cast<const uint16_t*>(a.k1) + kb, g.k.t, s, key0, s.nk, g.d, tid);
-      diff_load_keys<kOwn, D, kLoaders>(so + TK::BYTES, static_cast<const uint16_t*>(a.k2) + kb, g.k.t, s, key0, s.nk, g.d, tid);
-      diff_load_keys<kOwn, DV, kLoaders>(so + 2 * TK::BYTES, static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h, g.v.t, s, key0,
-                                         s.nk, g.dv, tid);
+      diff_clear<D, DV, kLoaders>(smem, Lay::OFF_X, g, tid);
+      diff_load_keys<kOwn, D, DV, kLoaders>(so, static_cast<const uint16_t*>(a.k1) + kb, static_cast<const uint16_t*>(a.k2) + kb,
+                                            static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h, g, s, key0, s.nk, tid);
       cp_async_commit();
     }
     for (int i = 0; i < n; ++i) {
@@ -502,11 +501,9 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
       }
       const uint32_t b = sst + st * Lay::STAGE;
       const int r0 = (j0 + i) * kStream;
-      diff_load_queries<kStream, D, kLoaders>(b, q1, g.q, g, s, r0, rows, g.d, tid);
-      diff_load_queries<kStream, D, kLoaders>(b + TQ::BYTES, q2, g.q, g, s, r0, rows, g.d, tid);
-      diff_load_queries<kStream, DV, kLoaders>(b + 2 * TQ::BYTES, dO, g.o, g, s, r0, rows, g.dv, tid);
-      if (tid < kRowArrays * kStream / 4)   // 16 pieces of 4 rows an array; rows_pad covers the last tile
-        cp_async_16_or_zero(b + 2 * TQ::BYTES + TO::BYTES + tid * 16, consts + (tid / 16) * a.row_stride + r0 + (tid % 16) * 4, true);
+      diff_load_queries<kStream, D, DV, kLoaders>(b, q1, q2, dO, g, s, r0, rows, tid);
+      for (int c = tid; c < kRowArrays * kStream / 4; c += kLoaders)   // 16 pieces of 4 rows an array; rows_pad covers the last tile
+        cp_async_16(smem + (b - so) + 2 * TQ::BYTES + TO::BYTES + c * 16, consts + (c / 16) * a.row_stride + r0 + (c % 16) * 4);
       cp_async_commit();
       cp_async_wait<1>();
       tell(i);
