@@ -498,7 +498,8 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* desc, const void*
  * lower edge are cut off there). */
 typedef struct {
   int batch, q_len, k_len;
-  int q_heads, kv_heads;    /* q_heads a multiple of kv_heads */
+  int q_heads, kv_heads;    /* q_heads a multiple of kv_heads, at most 64 of
+                               them to one */
   int d, dv;                /* widths of queries and keys (<= 64) and of values
                                (<= 128), multiples of 8 */
   rib_dtype dtype;          /* of every tensor but lam: RIB_BF16 or RIB_F16 */
@@ -507,14 +508,15 @@ typedef struct {
   int causal;               /* query t sees the keys up to t + keys - q_len */
   int window, width;        /* both 0: sequences; window <= 1024 */
   /* elements between batch items, tokens and heads; three zeros: contiguous.
-   * Multiples of 8. q: q1, q2 and their gradients, k: k1, k2, v: v, o: o, o2
-   * and dO. What is written may not overlap. */
+   * Multiples of 8, positive where the axis is longer than 1. q: q1, q2 and
+   * their gradients, k: k1, k2, v: v, o: o, o2 and dO. What is written may not
+   * overlap. */
   long long q_stride[3], k_stride[3], v_stride[3], o_stride[3];
 } rib_diff_attn_desc;
 
 /* Forward. lam [q_heads]. k_lens: int32 [batch], keys of each item (clamped to
- * 0..k_len), or NULL for k_len each; keys behind the length are never read,
- * and a row that sees no key gets o = 0 and lse = -inf. For the backward: o2
+ * 0..k_len), or NULL for k_len each; keys behind the length do not count,
+ * whatever they hold, and a row that sees no key gets o = 0 and lse = -inf. For the backward: o2
  * (the second map's output, layout of o) and lse fp32 [2][batch][q_heads]
  * [q_len] (natural logarithm, both maps); else NULL. Scores, softmax sums and
  * both maps' outputs are fp32; the probabilities take dtype for the product

@@ -139,10 +139,10 @@ ATTN_BWD = [P] * 5 + [P, None] + [P] * 10 + [P, 1 << 30, None]      # ..., o, o2
     ({"scale": float("inf")}, INVALID), ({"dtype_code": 1}, INVALID), ({"dtype_code": 7}, INVALID), ({"lam_code": 2}, INVALID),
     ({"window": 8}, INVALID), ({"width": 8}, INVALID), ({"window": -1, "width": 8}, INVALID), ({"window": 8, "width": 10}, INVALID),
     ({"window": 8, "width": 8, "k_len": 70}, INVALID), ({"window": 8, "width": 10, "k_len": 70, "causal": True}, INVALID),
-    ({"window": 1025, "width": 10, "k_len": 70}, UNSUPPORTED), ({"q_len": 1 << 30, "kv_heads": 1}, UNSUPPORTED),
+    ({"window": 1025, "width": 10, "k_len": 70}, UNSUPPORTED), ({"q_len": 0x7FFFFFFF}, UNSUPPORTED), ({"q_heads": 130}, UNSUPPORTED),
     ({"batch": 1 << 30}, UNSUPPORTED), ({"k_len": 0x7FFFFFFF}, UNSUPPORTED),
-    ({"q_stride": (4480, 64, 4)}, ALIGNMENT), ({"k_stride": (-8, 32, 16)}, ALIGNMENT), ({"o_stride": (0, 128, 32)}, INVALID),
-    ({"o_stride": (8960, 32, 32)}, INVALID),
+    ({"q_stride": (4480, 64, 4)}, ALIGNMENT), ({"k_stride": (-8, 32, 16)}, ALIGNMENT), ({"o_stride": (0, 128, 32)}, UNSUPPORTED),
+    ({"o_stride": (8960, 32, 32)}, INVALID), ({"k_stride": (2880, 1 << 32, 16)}, UNSUPPORTED),
 ], ids=str)
 def test_diff_attention_descriptor_refusals(lib, kw, st):
     d = _attn(**kw)
@@ -170,10 +170,10 @@ def test_diff_attention_argument_refusals(lib):
     w = dict(window=8, width=10, k_len=70)
     assert f(_attn(**w), _with(ATTN, _6=P)) == INVALID and b(_attn(**w), _with(ATTN_BWD, _6=P)) == INVALID   # windows and lengths
     assert b(_attn(), _with(ATTN_BWD, _18=100)) == INVALID                                                   # workspace too small
-    # gradients that would lie on one another; a broadcast input is fine in the forward
+    # gradients that would lie on one another
     for k in ("q_stride", "k_stride"):
-        assert b(_attn(**{k: (0, 64, 16)}), ATTN_BWD) == INVALID
-    assert b(_attn(v_stride=(0, 64, 32)), ATTN_BWD) == INVALID
+        assert b(_attn(**{k: (64, 64, 16)}), ATTN_BWD) == INVALID
+    assert b(_attn(v_stride=(5760, 32, 32)), ATTN_BWD) == INVALID
     long = dict(batch=1, q_len=1, k_len=100000)
     assert lib.rib_diff_attention_workspace_size(_attn(**long)) > 0
     assert f(_attn(**long), _with(ATTN, _10=None)) == INVALID and f(_attn(**long), _with(ATTN, _11=64)) == INVALID

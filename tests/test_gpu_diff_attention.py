@@ -168,7 +168,7 @@ def _check(rib, B, Nq, Nk, Hq, Hk, d, dv, t, lens=None, train=True, rms=(), lam_
 
 
 ALL = ("o", "o2", "dq1", "dq2", "dk1", "dk2", "dv")
-WIDTHS = [(16, 32), (8, 8), (24, 40), (32, 64), (16, 64), (64, 64), (64, 128), (40, 16), (48, 104)]
+WIDTHS = [(16, 32), (8, 8), (32, 64), (24, 40), (24, 64), (32, 40), (16, 64), (64, 128), (64, 64), (40, 16), (48, 104)]
 
 
 @pytest.mark.parametrize("t", [BF16, F16])

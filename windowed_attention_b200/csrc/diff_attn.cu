@@ -5,6 +5,7 @@
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 
 #include "diff_attn.cuh"
 
@@ -18,11 +19,24 @@ rib_status bad(const char* who, rib_status st, const char* what) {
 }
 
 // The strides of a tensor [batch][tokens][heads][e]; all zero means contiguous.
-DiffStrides strides(const long long (&s)[3], long long tokens, int heads, int e) {
+struct Strides { long long b, t, h; };
+Strides strides(const long long (&s)[3], long long tokens, int heads, int e) {
   if (!s[0] && !s[1] && !s[2]) return {tokens * heads * e, static_cast<long long>(heads) * e, e};
   return {s[0], s[1], s[2]};
 }
-bool bad_strides(const DiffStrides& s) { return s.b < 0 || s.t < 0 || s.h < 0 || s.b % 8 || s.t % 8 || s.h % 8; }
+// The kernels' form of them; token and head strides are ints there.
+rib_status narrow(const char* who, const Strides& s, const long long (&n)[3], int rows, DiffStrides* out) {
+  if (s.b < 0 || s.t < 0 || s.h < 0 || s.b % 8 || s.t % 8 || s.h % 8)
+    return bad(who, RIB_ERR_ALIGNMENT, "strides must be non-negative multiples of 8 elements");
+  // a tensor map holds strides below 2^40 bytes (a map's row: width tokens)
+  if (s.t > 0x7FFFFFFF || s.h > 0x7FFFFFFF || s.b >= (1ll << 39) || s.t * rows >= (1ll << 39))
+    return bad(who, RIB_ERR_UNSUPPORTED, "token or head stride of 2^31 elements, or batch stride of 2^39, or more");
+  // an axis that is stepped along needs a stride of its own
+  if (n[0] > 0 && n[1] > 0 && ((n[0] > 1 && s.b == 0) || (n[1] > 1 && s.t == 0) || (n[2] > 1 && s.h == 0)))
+    return bad(who, RIB_ERR_UNSUPPORTED, "a stride of 0 (a broadcast tensor): give its one copy as an axis of length 1");
+  *out = {s.b, static_cast<int>(s.t), static_cast<int>(s.h)};
+  return RIB_OK;
+}
 // Written tensors may not lay two values on one place: the head stride holds a
 // row of e, the token stride a token's heads and the batch stride an item.
 bool overlaps(const DiffStrides& s, int batch, long long tokens, int heads, int e) {
@@ -38,6 +52,33 @@ bool overlaps(const DiffStrides& s, int batch, long long tokens, int heads, int 
     reach += (x.n - 1) * x.st;
   }
   return false;
+}
+
+// Boxes of 64 rows. In a window: the power of two of columns that takes the
+// fewest boxes (the widest of them: longer runs of memory).
+void boxes(DiffGeom* g) {
+  const int tokens = 64 / g->group;
+  if (!g->window) {
+    g->tck = 64; g->lk = 6; g->trk = 1;
+    g->tcq = tokens; g->lq = 31; g->trq = 1;
+    return;
+  }
+  const int w = diff_span_x(*g, 0), h = diff_span_y(*g);
+  auto pick = [&](int n, int* tc, int* l, int* tr) {
+    int top = 0;
+    while ((2 << top) <= n) ++top;   // the largest power of two within n
+    long long best = -1;
+    for (int i = 0; i <= top; ++i) {
+      const int c = 1 << i, r = 1 << (top - i);
+      const long long count = static_cast<long long>(ceil_div(w, c)) * ceil_div(h > 0 ? h : 1, r);
+      if (best < 0 || count <= best) {
+        best = count;
+        *tc = c; *l = i; *tr = r;
+      }
+    }
+  };
+  pick(64, &g->tck, &g->lk, &g->trk);
+  pick(tokens, &g->tcq, &g->lq, &g->trq);
 }
 
 rib_status geometry(const char* who, const rib_diff_attn_desc* d, DiffGeom* g) {
@@ -70,21 +111,21 @@ rib_status geometry(const char* who, const rib_diff_attn_desc* d, DiffGeom* g) {
   g->group_magic = div_magic(static_cast<uint32_t>(g->group));
   g->scale = d->scale;
   g->scale_log2 = d->scale * kDiffLog2e;
-  g->q = strides(d->q_stride, d->q_len, d->q_heads, d->d);
-  g->k = strides(d->k_stride, d->k_len, d->kv_heads, d->d);
-  g->v = strides(d->v_stride, d->k_len, d->kv_heads, d->dv);
-  g->o = strides(d->o_stride, d->q_len, d->q_heads, d->dv);
-  // rows are ints (with a tile behind the last), and row / group is exact below 2^32
-  const long long rows = static_cast<long long>(d->q_len) * g->group;
-  if (rows > 0x7FFFFFFFll - 256 || rows > 0xFFFFFFFFll / g->group - 256 || d->k_len > 0x7FFFFFFF - 256 || d->q_len > 0x7FFFFFFF - 256)
-    return bad(who, RIB_ERR_UNSUPPORTED, "sequences too long");
+  rib_status st = RIB_OK;
+  if ((st = narrow(who, strides(d->q_stride, d->q_len, d->q_heads, d->d), {d->batch, d->q_len, d->q_heads}, d->window ? d->width : 1, &g->q)) != RIB_OK ||
+      (st = narrow(who, strides(d->k_stride, d->k_len, d->kv_heads, d->d), {d->batch, d->k_len, d->kv_heads}, d->window ? d->width : 1, &g->k)) != RIB_OK ||
+      (st = narrow(who, strides(d->v_stride, d->k_len, d->kv_heads, d->dv), {d->batch, d->k_len, d->kv_heads}, d->window ? d->width : 1, &g->v)) != RIB_OK ||
+      (st = narrow(who, strides(d->o_stride, d->q_len, d->q_heads, d->dv), {d->batch, d->q_len, d->q_heads}, d->window ? d->width : 1, &g->o)) != RIB_OK)
+    return st;
+  if (g->group > 64) return bad(who, RIB_ERR_UNSUPPORTED, "more than 64 query heads a key head");
+  // coordinates and tokens are ints, with a box behind the last
+  if (d->q_len > 0x7FFFFFFF - 256 || d->k_len > 0x7FFFFFFF - 256) return bad(who, RIB_ERR_UNSUPPORTED, "sequences too long");
+  boxes(g);
   // units of work are ints: (sequences, key heads, tiles, splits)
   const long long seqs = static_cast<long long>(d->batch) * (d->window ? static_cast<long long>(g->nwx) * g->nwy : 1);
-  const long long tiles = (diff_max_rows(*g) > diff_max_keys(*g) ? diff_max_rows(*g) : diff_max_keys(*g)) / 32 + 1;
-  if (seqs > 0x7FFFFFFFll / d->kv_heads || seqs * d->kv_heads > 0x3FFFFFFFll / (tiles > 64 ? tiles : 64))
+  const long long bq = diff_max_q_boxes(*g), bk = diff_max_k_boxes(*g), tiles = (bq > bk ? bq : bk) + 64;
+  if (seqs > 0x7FFFFFFFll / d->kv_heads || seqs * d->kv_heads > 0x3FFFFFFFll / tiles)
     return bad(who, RIB_ERR_UNSUPPORTED, "too many sequences and heads");
-  if (bad_strides(g->q) || bad_strides(g->k) || bad_strides(g->v) || bad_strides(g->o))
-    return bad(who, RIB_ERR_ALIGNMENT, "strides must be non-negative multiples of 8 elements");
   if (overlaps(g->o, d->batch, d->q_len, d->q_heads, d->dv)) return bad(who, RIB_ERR_INVALID_ARG, "o_stride lays values of o on one another");
   return RIB_OK;
 }
@@ -97,7 +138,11 @@ bool misaligned(std::initializer_list<const void*> ps, uintptr_t to) {
 
 uintptr_t lam_size(const rib_diff_attn_desc* d) { return d->lam_dtype == RIB_F32 ? 4 : 2; }
 
-long long row_values(const DiffGeom& g) { return static_cast<long long>(diff_sequences(g)) * g.kv_heads * diff_rows_pad(g); }
+// Query boxes of one (sequence, key head) in the backward's row constants: whole tiles of two.
+int row_boxes(const DiffGeom& g) { return ceil_div(diff_max_q_boxes(g), 2) * 2; }
+size_t row_bytes(const DiffGeom& g) {
+  return static_cast<size_t>(diff_sequences(g)) * g.kv_heads * row_boxes(g) * kRowArrays * 64 * sizeof(float);
+}
 
 }  // namespace
 }  // namespace rib
@@ -140,7 +185,7 @@ rib_status rib_diff_attention(const rib_diff_attn_desc* d, const void* q1, const
 
 size_t rib_diff_attention_bwd_workspace_size(const rib_diff_attn_desc* d) {
   DiffGeom g;
-  return geometry("rib_diff_attention_bwd_workspace_size", d, &g) == RIB_OK ? row_values(g) * kRowArrays * sizeof(float) : 0;
+  return geometry("rib_diff_attention_bwd_workspace_size", d, &g) == RIB_OK ? row_bytes(g) : 0;
 }
 
 rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, const void* q2, const void* k1, const void* k2, const void* v,
@@ -163,10 +208,8 @@ rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, c
   if (overlaps(g.q, d->batch, d->q_len, d->q_heads, d->d) || overlaps(g.k, d->batch, d->k_len, d->kv_heads, d->d) ||
       overlaps(g.v, d->batch, d->k_len, d->kv_heads, d->dv))
     return bad(who, RIB_ERR_INVALID_ARG, "strides lay gradients on one another");
-  a.rows_pad = static_cast<int>(diff_rows_pad(g));
-  a.row_stride = row_values(g);
-  if (rows && (!ws || ws_bytes < a.row_stride * kRowArrays * sizeof(float)))
-    return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
+  a.boxes = row_boxes(g);
+  if (rows && (!ws || ws_bytes < row_bytes(g))) return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
   a.rows = static_cast<float*>(ws);
   a.g.k_lens = k_lens;
   a.q1 = q1; a.q2 = q2; a.k1 = k1; a.k2 = k2; a.v = v; a.lam = lam; a.o = o; a.o2 = o2; a.lse = lse; a.dO = dO;

@@ -2,11 +2,17 @@
 // and how their rows reach the swizzled shared-memory tiles that tcgen05.mma
 // reads.
 //
-// A sequence is one batch item (window 0) or one window of a map, cut off at
-// the map's edge. Query rows are (token, query head of the group) pairs,
-// row = token * G + g: the G query heads that share a key head meet the same
-// key tiles, so a tile of 128 rows is full even for a single token with many
-// heads, and the gradients of a shared head are sums over rows.
+// A sequence is one batch item, or one window of a map, cut off at the map's
+// edge. Both are rectangles of tokens (a sequence is one row of them), and TMA
+// loads a rectangle of at most 64 rows, a "box":
+//   keys     64 tokens, tck x trk
+//   queries  tcq x trq tokens times the G query heads that share a key head,
+//            row = token * G + head: boxes are full even for single tokens of
+//            many heads, and gradients of a shared head are sums over rows.
+// The order of a window's tokens does not matter to attention, so boxes need
+// not follow it. Rows of a box outside the sequence are masked; where they
+// hold other tokens (a neighbouring window, keys behind a length) the streamed
+// side's are also cleared, since 0 * NaN is NaN in a product.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -20,13 +26,16 @@ constexpr float kDiffLog2e = 1.4426950408889634f;
 constexpr float kDiffLn2 = 0.6931471805599453f;
 
 struct DiffStrides {
-  long long b, t, h;   // elements between batch items, tokens and heads
+  long long b;   // elements between batch items,
+  int t, h;      // tokens and heads
 };
 
 struct DiffGeom {
   int batch, q_len, k_len, q_heads, kv_heads, group;   // group = q_heads / kv_heads
   int d, dv;
   int window, width, height, nwx, nwy;                 // window 0: sequences
+  int tck, lk, trk;                                    // key boxes; lk = log2 tck
+  int tcq, lq, trq;                                    // query boxes; lq = log2 tcq, 31 for sequences (one row)
   int causal, lam_f32;
   uint32_t group_magic;                                // see div_by(); 0: group 1
   float scale, scale_log2;
@@ -39,20 +48,13 @@ __host__ __device__ inline uint32_t div_magic(uint32_t n) { return n > 1 ? 0xFFF
 __device__ __forceinline__ int div_by(int t, uint32_t magic) {
   return static_cast<int>(__umulhi(static_cast<uint32_t>(t), magic));
 }
+__host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
+__device__ __forceinline__ long long wide(int a, int b) { return static_cast<long long>(a) * b; }
 
-// Query row r is (token r / G, head r % G of the group).
-__device__ __forceinline__ int diff_row_token(const DiffGeom& g, int r) { return g.group_magic ? div_by(r, g.group_magic) : r; }
-
-// One sequence: token t (0 .. nq - 1 of the queries, 0 .. nk - 1 of the keys)
-// is batch item b's token t0 + (t / n1) * width + t % n1.
+// One sequence: a rectangle of queries wq x hq and one of keys wk x hk at (x0, y0) of batch item b.
 struct DiffSeq {
-  int b, t0, nq, nk, n1, width;
-  uint32_t magic;   // of n1; 0 with one column (n1 = 1) or a sequence (n1 = 0)
-
-  __device__ __forceinline__ long long token(int t) const {
-    const int r = magic ? div_by(t, magic) : (n1 == 1 ? t : 0);
-    return static_cast<long long>(t0) + static_cast<long long>(r) * width + (t - r * n1);
-  }
+  int b, x0, y0, wq, hq, wk, hk, width;
+  __device__ __forceinline__ int token(int x, int y) const { return (y0 + y) * width + x0 + x; }
 };
 
 __device__ __forceinline__ DiffSeq diff_sequence(const DiffGeom& g, int s) {
@@ -60,29 +62,77 @@ __device__ __forceinline__ DiffSeq diff_sequence(const DiffGeom& g, int s) {
   if (g.window) {
     const int wx = s % g.nwx, wy = (s / g.nwx) % g.nwy;
     q.b = s / (g.nwx * g.nwy);
-    const int y0 = wy * g.window, x0 = wx * g.window;
-    const int hv = min(g.window, g.height - y0), wv = min(g.window, g.width - x0);
-    q.t0 = y0 * g.width + x0;
-    q.nq = q.nk = hv * wv;
-    q.n1 = wv;
+    q.x0 = wx * g.window;
+    q.y0 = wy * g.window;
+    q.wq = q.wk = min(g.window, g.width - q.x0);
+    q.hq = q.hk = min(g.window, g.height - q.y0);
     q.width = g.width;
-    q.magic = div_magic(static_cast<uint32_t>(wv));
   } else {
     q.b = s;
-    q.t0 = 0;
-    q.nq = g.q_len;
-    q.nk = g.k_lens ? min(max(g.k_lens[s], 0), g.k_len) : g.k_len;
-    q.n1 = 0;
+    q.x0 = q.y0 = 0;
+    q.wq = g.q_len;
+    q.wk = g.k_lens ? min(max(g.k_lens[s], 0), g.k_len) : g.k_len;
+    q.hq = q.hk = 1;
     q.width = 0;
-    q.magic = 0u;
   }
   return q;
 }
 
-// Keys that query token t of a sequence sees (a prefix): all, or with the
-// causal mask those up to its own place counted from the end.
-__device__ __forceinline__ int diff_visible(const DiffGeom& g, const DiffSeq& s, int t) {
-  return g.causal ? min(max(t + 1 + s.nk - s.nq, 0), s.nk) : s.nk;
+// Keys that query x of a sequence sees (a prefix; windows see all, see below):
+// with the causal mask those up to its own place counted from the end.
+__device__ __forceinline__ int diff_visible(const DiffGeom& g, const DiffSeq& s, int x) {
+  return g.causal ? min(max(x + 1 + s.wk - s.wq, 0), s.wk) : s.wk;
+}
+__device__ __forceinline__ int diff_q_boxes(const DiffGeom& g, const DiffSeq& s) {
+  return ceil_div(s.wq, g.tcq) * ceil_div(s.hq, g.trq);
+}
+
+// Row r6 of a query box.
+struct DiffRow {
+  int x, y, head;   // place in the sequence; head in its group
+  bool live;
+};
+__device__ __forceinline__ DiffRow diff_query_row(const DiffGeom& g, const DiffSeq& s, int box, int r6) {
+  DiffRow r;
+  const int idx = g.group_magic ? div_by(r6, g.group_magic) : r6;
+  r.head = r6 - idx * g.group;
+  const int nx = ceil_div(s.wq, g.tcq), by = box / nx, bx = box - by * nx;
+  const int yy = idx >> g.lq, xx = idx - (yy << g.lq);
+  r.x = bx * g.tcq + xx;
+  r.y = by * g.trq + yy;
+  r.live = idx < g.tcq * g.trq && r.x < s.wq && r.y < s.hq;
+  return r;
+}
+
+// The keys of box j that exist, a bit each: column c is (c % tck, c / tck) of the box.
+struct DiffKeyBox {
+  int x, y, vx, vy;   // place in the sequence, existing columns and rows (vx may exceed tck, vy trk)
+};
+__device__ __forceinline__ DiffKeyBox diff_key_box(const DiffGeom& g, const DiffSeq& s, int nx, int j) {
+  DiffKeyBox k;
+  const int by = j / nx, bx = j - by * nx;
+  k.x = bx * g.tck;
+  k.y = by * g.trk;
+  k.vx = s.wk - k.x;
+  k.vy = s.hk - k.y;
+  return k;
+}
+__device__ __forceinline__ uint64_t diff_key_mask(const DiffGeom& g, int vx, int vy) {
+  if (vx <= 0 || vy <= 0) return 0ull;
+  const uint64_t row = vx >= g.tck ? (g.tck == 64 ? ~0ull : (1ull << g.tck) - 1ull) : (1ull << vx) - 1ull;
+  uint64_t m = 0ull;
+  for (int y = 0; y < min(vy, g.trk); ++y) m |= row << (y << g.lk);
+  return m;
+}
+
+// The keys of box j that a row sees which sees `seen` keys of its sequence.
+__device__ __forceinline__ uint64_t diff_seen(const DiffGeom& g, const DiffSeq& s, int nx, int j, int seen) {
+  if (g.window) {
+    const DiffKeyBox k = diff_key_box(g, s, nx, j);
+    return diff_key_mask(g, k.vx, k.vy);
+  }
+  const int left = seen - 64 * j;
+  return left >= 64 ? ~0ull : (left > 0 ? (1ull << left) - 1ull : 0ull);
 }
 
 // A tile of ROWS rows of D 16-bit elements as tcgen05.mma operands: atoms of up
@@ -97,7 +147,6 @@ struct DiffTile {
   static constexpr int ATOM = ROWS * RB;
   static constexpr int BYTES = ROWS * D * 2;
   static constexpr uint32_t SW = RB == 128 ? SW_128B : (RB == 64 ? SW_64B : SW_32B);
-  static constexpr int CHUNKS = D / 8;   // 16-byte pieces of a row
   static_assert(D == 16 || D == 32 || D == 64 || D == 128, "operand widths");
 
   __device__ static __forceinline__ uint32_t offset(int row, int chunk) {
@@ -106,78 +155,42 @@ struct DiffTile {
     const int x = RB == 128 ? (row & 7) : (RB == 64 ? ((row >> 1) & 3) : ((row >> 2) & 1));
     return static_cast<uint32_t>(a * ATOM + row * RB + ((c ^ x) << 4));
   }
-  // K-major descriptor of K step ks (16 columns)
-  __device__ static __forceinline__ uint64_t kmajor(uint32_t base, int ks) {
-    constexpr int per = COLS / 16;
-    return make_sdesc(base + (ks / per) * ATOM + (ks % per) * 32, 16, 8 * RB, SW);
+  // Descriptors of a tile at shared address `base`, and what K step ks adds to
+  // them (a descriptor's low bits are the address / 16): one addition a
+  // product, since the issuing thread's own instructions bound its rate.
+  // K-major: steps of 16 columns; MN-major: steps of 16 rows.
+  __device__ static __forceinline__ uint64_t kmajor(uint32_t base) { return make_sdesc(base, 16, 8 * RB, SW); }
+  __device__ static constexpr uint32_t kstep(int ks) { return (ks / (COLS / 16) * ATOM + ks % (COLS / 16) * 32) >> 4; }
+  __device__ static __forceinline__ uint64_t mnmajor(uint32_t base) { return make_sdesc(base, ATOM, 8 * RB, SW); }
+  __device__ static constexpr uint32_t mnstep(int ks) { return (ks * 16 * RB) >> 4; }
+  // One box into rows 64 half .. of the tile; columns behind the tensor's width
+  // arrive as zeros.
+  __device__ static __forceinline__ void load(uint8_t* tile, int half, const CUtensorMap* map, uint64_t* bar, int head, int x, int y, int b) {
+#pragma unroll
+    for (int a = 0; a < D / COLS; ++a) tma_load_5d(tile + a * ATOM + half * 64 * RB, map, bar, a * COLS, head, x, y, b);
   }
-  // MN-major descriptor of K step ks (16 rows)
-  __device__ static __forceinline__ uint64_t mnmajor(uint32_t base, int ks) {
-    return make_sdesc(base + ks * 16 * RB, ATOM, 8 * RB, SW);
+  __device__ static __forceinline__ uint32_t box_bytes(int rows) { return static_cast<uint32_t>(rows * D * 2); }
+  // Zeros into a row, by `lanes` threads.
+  __device__ static __forceinline__ void clear_row(uint8_t* tile, int row, int lane, int lanes) {
+    for (int c = lane; c < D / 8; c += lanes) *reinterpret_cast<uint4*>(tile + offset(row, c)) = make_uint4(0u, 0u, 0u, 0u);
   }
 };
 
-// One row of a tensor into a tile, by a pair of lanes (par = 0, 1: they share
-// 32-byte sectors): two instructions a 16-byte piece, since the swizzle is an
-// exclusive or of the row's place. `size` is 16, or 0 for a row of zeros (src is
-// not read then). Pieces at or behind n (the tensor's width) are left as they are.
-template <int ROWS, int D>
-__device__ __forceinline__ void diff_load_row(uint32_t tile, int row, int par, const uint16_t* src, int size, int n) {
-  using T = DiffTile<ROWS, D>;
-  constexpr int per = T::COLS / 8;
-  const uint32_t dst = tile + T::offset(row, par);
-  const uint16_t* from = src + par * 8;
-#pragma unroll
-  for (int k = 0; k < T::CHUNKS / 2; ++k)
-    if (2 * k + par < n)
-      asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
-                   ::"r"((dst ^ ((2 * k % per) << 4)) + 2 * k / per * T::ATOM), "l"(from + 16 * k), "r"(size) : "memory");
-}
-
-// Rows first .. first + ROWS - 1 of the key side (a row a token): k1, k2 and v
-// into three tiles one behind the other. Rows at or behind n become zero, so
-// what a mask hides never reaches a product. Every row is a pair of lanes.
-template <int ROWS, int D, int DV, int THREADS>
-__device__ __forceinline__ void diff_load_keys(uint32_t tile, const uint16_t* k1, const uint16_t* k2, const uint16_t* v, const DiffGeom& g,
-                                               const DiffSeq& s, int first, int n, int tid) {
-  const int par = tid & 1, nd = g.d / 8, nv = g.dv / 8;
-#pragma unroll
-  for (int row = tid >> 1; row < ROWS; row += THREADS / 2) {
-    const int t = first + row, size = t < n ? 16 : 0;
-    const long long token = t < n ? s.token(t) : 0;
-    diff_load_row<ROWS, D>(tile, row, par, k1 + token * g.k.t, size, nd);
-    diff_load_row<ROWS, D>(tile + DiffTile<ROWS, D>::BYTES, row, par, k2 + token * g.k.t, size, nd);
-    diff_load_row<ROWS, DV>(tile + 2 * DiffTile<ROWS, D>::BYTES, row, par, v + token * g.v.t, size, nv);
-  }
-}
-
-// The same for the query side: q1, q2 and (dO not null) dO.
-template <int ROWS, int D, int DV, int THREADS>
-__device__ __forceinline__ void diff_load_queries(uint32_t tile, const uint16_t* q1, const uint16_t* q2, const uint16_t* dO, const DiffGeom& g,
-                                                  const DiffSeq& s, int first, int n, int tid) {
-  const int par = tid & 1, nd = g.d / 8, nv = g.dv / 8;
-#pragma unroll
-  for (int row = tid >> 1; row < ROWS; row += THREADS / 2) {
-    const int r = first + row, size = r < n ? 16 : 0;
-    const int t = r < n ? diff_row_token(g, r) : 0, h = r < n ? r - t * g.group : 0;
-    const long long token = s.token(t), at = token * g.q.t + h * g.q.h;
-    diff_load_row<ROWS, D>(tile, row, par, q1 + at, size, nd);
-    diff_load_row<ROWS, D>(tile + DiffTile<ROWS, D>::BYTES, row, par, q2 + at, size, nd);
-    if (dO) diff_load_row<ROWS, DV>(tile + 2 * DiffTile<ROWS, D>::BYTES, row, par, dO + token * g.o.t + h * g.o.h, size, nv);
-  }
-}
-
-// Zeros for the columns behind the tensors' widths, which no load writes: the
-// loader warps clear their tiles once (barrier 2 is theirs).
-template <int D, int DV, int THREADS>
-__device__ __forceinline__ void diff_clear(uint8_t* tiles, int bytes, const DiffGeom& g, int tid) {
-  if (g.d == D && g.dv == DV) return;
-  for (int i = tid * 16; i < bytes; i += THREADS * 16) *reinterpret_cast<uint4*>(tiles + i) = make_uint4(0u, 0u, 0u, 0u);
-  asm volatile("bar.sync 2, %0;" ::"n"(THREADS) : "memory");
-}
-
 __host__ __device__ constexpr uint32_t diff_idesc(bool f16, int N, bool b_mn) {
   return f16 ? idesc_f16(128, N, false, b_mn) : idesc_bf16(128, N, false, b_mn);
+}
+
+// D = A B^T over every K step of two K-major tiles (columns behind the
+// tensors' width are zeros).
+template <typename TA, typename TB, int STEPS>
+__device__ __forceinline__ void diff_mma_kk(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+#pragma unroll
+  for (int ks = 0; ks < STEPS; ++ks) umma_ss(d, a + TA::kstep(ks), b + TB::kstep(ks), idesc, ks > 0 ? 1u : 0u);
+}
+
+// A bounded wait of a whole warp.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, const WaitCtx& w, int site) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, w, site));
 }
 
 // 2^x for a pair of x in [-inf, 127] on the FMA pipe, for the share of the
@@ -231,33 +244,33 @@ struct DiffFwdArgs {
   int splits;
   int* err;
 };
-// Row constants of the backward, one array each, for the query rows of every
-// (sequence, key head) padded to a multiple of 128: -log2e lse1, -log2e lse2,
-// -dO.O1, -dO.O2, -lambda and the keys that the row sees (an int; 0 for the padding).
-enum { kRowL1 = 0, kRowL2, kRowD1, kRowD2, kRowLam, kRowSeen, kRowArrays };
+// Row constants of the backward, for every box of 64 query rows of every
+// (sequence, key head), [boxes][kRowArrays][64]: -log2e lse1, -log2e lse2,
+// -dO.O1, -dO.O2, -lambda, and what dlambda sums (-sum_k P2 dP, by the dq
+// kernel). Rows without a query: -inf, -inf and zeros, so that P = 0.
+enum { kRowL1 = 0, kRowL2, kRowD1, kRowD2, kRowLam, kRowSum, kRowArrays };
 struct DiffBwdArgs {
   DiffGeom g;
   const void *q1, *q2, *k1, *k2, *v, *lam, *o, *o2, *dO;
   const float* lse;
   void *dq1, *dq2, *dk1, *dk2, *dv, *dlam;
-  float* rows;       // [kRowArrays][row_stride]
-  long long row_stride;
-  int rows_pad;      // rows of one (sequence, key head)
+  float* rows;
+  int boxes;         // of one (sequence, key head), an even number
   int* err;
 };
 inline int diff_sequences(const DiffGeom& g) { return g.window ? g.batch * g.nwx * g.nwy : g.batch; }
-// Query rows of the longest sequence, of one key head.
-inline long long diff_max_rows(const DiffGeom& g) {
-  const long long nq = g.window ? static_cast<long long>(g.window < g.height ? g.window : g.height) * (g.window < g.width ? g.window : g.width)
-                                : g.q_len;
-  return nq * g.group;
-}
-inline int diff_max_keys(const DiffGeom& g) { return g.window ? static_cast<int>(diff_max_rows(g) / g.group) : g.k_len; }
+// The longest sequence's extents and boxes.
+inline int diff_span_x(const DiffGeom& g, int len) { return g.window ? (g.window < g.width ? g.window : g.width) : len; }
+inline int diff_span_y(const DiffGeom& g) { return g.window ? (g.window < g.height ? g.window : g.height) : 1; }
+inline int diff_max_q_boxes(const DiffGeom& g) { return ceil_div(diff_span_x(g, g.q_len), g.tcq) * ceil_div(diff_span_y(g), g.trq); }
+inline int diff_max_k_boxes(const DiffGeom& g) { return ceil_div(diff_span_x(g, g.k_len), g.tck) * ceil_div(diff_span_y(g), g.trk); }
 // The operand widths of the kernels: the smallest pair that holds d and dv.
 inline int diff_class(int d, int dv) { return d <= 16 && dv <= 32 ? 0 : (d <= 32 && dv <= 64 ? 1 : 2); }
 int diff_splits(const DiffGeom& g);
 size_t diff_split_bytes(const DiffGeom& g);
-long long diff_rows_pad(const DiffGeom& g);
+// Tensor maps (columns, heads, x, y, batch) of the query and the key side with
+// their boxes; `cols` is the width of an operand atom.
+bool diff_map(CUtensorMap* map, const DiffGeom& g, bool query, bool f16, const void* p, const DiffStrides& s, int e, int cols);
 cudaError_t launch_diff_attn_fwd(const DiffFwdArgs& a, bool f16, cudaStream_t stream);
 cudaError_t launch_diff_attn_bwd(const DiffBwdArgs& a, bool f16, cudaStream_t stream);
 

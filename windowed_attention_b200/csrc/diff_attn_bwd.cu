@@ -4,20 +4,25 @@
 //   D_i = rowsum(dO * O_i),            O_1 = O + lambda O_2
 //   dS_1 = P_1 (dP - D_1),             dS_2 = -lambda P_2 (dP - D_2)
 //   dQ_i = s dS_i K_i,  dK_i = s dS_i^T Q_i,  dV = (P_1 - lambda P_2)^T dO
-//   dlambda = -sum over the head's rows of D_2
+//   dlambda = -sum over the head's rows of sum_k P_2 dP
 // P_i is formed again from the forward's log-sum-exps. Gradients of a key head
 // that several query heads share are sums over its rows, in one accumulator.
 //
 // Three launches:
-//  * rows: D_1, D_2 and the other row constants, one array each, so that the
-//    key-side kernel reads four neighbouring rows' with one load.
-//  * dq: one CTA owns 128 query rows and streams key tiles of 64.
-//  * dkv: one CTA owns 128 keys of a key head and streams tiles of 64 query
-//    rows, keys in the TMEM lanes (S_i^T = K_i Q_i^T); the last CTAs add up
-//    dlambda. Every sum has one owner and a fixed order: the same bits on
-//    every run, no atomics.
+//  * rows: D_1, D_2 and the other row constants, box by box of 64 query rows.
+//  * dq: one CTA owns 128 query rows and streams key boxes of 64. It also sums
+//    P_2 dP in fp32, which spares dlambda the rounding of a stored O_2.
+//  * dkv: one CTA owns 128 keys of a key head and streams query boxes, keys in
+//    the TMEM lanes (S_i^T = K_i Q_i^T); the last CTAs add up dlambda. Every
+//    sum has one owner and a fixed order: the same bits on every run, no
+//    atomics.
 // Both recompute S_i and dP: the alternative, one kernel that adds its dQ
 // tiles to memory, needs atomics, whose order changes the result.
+//
+// Roles in both: 16 elementwise warps (thread = TMEM lane; P and dS take the
+// 16-bit type for the products, half a step of each), two MMA issuers (scores;
+// gradients), a TMA producer, and a warp that clears the rows of a streamed
+// box that are not the sequence's.
 //
 // Bound: the exponentials (2 per pair and kernel, 16 a cycle and SM) at d <= 32;
 // with d = 64, dv = 128 the products, whose cost per 128 x 64 tile in cycles
@@ -29,14 +34,19 @@
 namespace rib {
 namespace {
 
+#ifndef RIB_DIFF_POLY_Q
+#define RIB_DIFF_POLY_Q 0
+#endif
+#ifndef RIB_DIFF_POLY_K
+#define RIB_DIFF_POLY_K 0
+#endif
 constexpr int kOwn = 128, kStream = 64;
-constexpr int kLoadWarps = 4;
-constexpr int kLoaders = 32 * kLoadWarps;
-constexpr int kThreads = 32 * (10 + kLoadWarps);   // 8 elementwise warps, two MMA issuers, the loaders
+constexpr int kWarpS = 16, kWarpX = 17, kWarpLoad = 18, kWarpClear = 19;
+constexpr int kThreads = 32 * 20;
 
 enum Site : int {
-  SITE_OWN = 421, SITE_ST_FULL = 422, SITE_ST_EMPTY = 423, SITE_S_FULL = 424, SITE_S_FREE = 425, SITE_X_FULL = 426, SITE_X_DONE = 427,
-  SITE_DONE = 428,
+  SITE_RAW = 420, SITE_OWN = 421, SITE_ST_FULL = 422, SITE_ST_EMPTY = 423, SITE_S_FULL = 424, SITE_S_FREE = 425, SITE_X_FULL = 426,
+  SITE_X_DONE = 427, SITE_DONE = 428,
 };
 
 // fp16 probabilities and their gradients are held times 2^6, which moves
@@ -48,23 +58,44 @@ constexpr float kShift = F16 ? 6.f : 0.f;
 template <bool F16>
 constexpr float kUnshift = F16 ? 1.f / 64.f : 1.f;
 
+template <bool POLY>
+__device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
+  float x0, x1, y0, y1;
+  f2_unpack(x, x0, x1);
+  if constexpr (POLY) {
+    diff_exp2_poly(x0, x1, y0, y1);
+  } else {
+    y0 = ex2_approx(x0);
+    y1 = ex2_approx(x1);
+  }
+  return f2_pack(y0, y1);
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
+  float x0, x1;
+  f2_unpack(x, x0, x1);
+  return diff_pack<F16>(x0, x1);
+}
+__device__ __forceinline__ uint64_t raw_pair(const uint32_t* r) { return f2_pack(__uint_as_float(r[0]), __uint_as_float(r[1])); }
+
 // ---------------------------------------------------------------- row constants
-// LPR lanes hold a row's eight columns each.
+// LPR lanes hold a row's eight columns each; a CTA takes rows of one box.
 template <int LPR, bool F16>
 __global__ void __launch_bounds__(256) diff_attn_rows_kernel(const DiffBwdArgs a) {
   const DiffGeom& g = a.g;
-  constexpr int kRows = 256 / LPR;
-  const int per = a.rows_pad / kRows, unit = blockIdx.x / per;
-  const int r = (blockIdx.x - unit * per) * kRows + threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  constexpr int kRows = 256 / LPR;   // 64, 32 or 16
+  const long long box_at = static_cast<long long>(blockIdx.x) * kRows / 64;
+  const int r6 = static_cast<int>(static_cast<long long>(blockIdx.x) * kRows % 64) + threadIdx.x / LPR, lane = threadIdx.x % LPR;
+  const int unit = static_cast<int>(box_at / a.boxes), box = static_cast<int>(box_at - static_cast<long long>(unit) * a.boxes);
   const int hk = unit % g.kv_heads;
   const DiffSeq s = diff_sequence(g, unit / g.kv_heads);
-  const bool live = r < s.nq * g.group;
-  const int t = live ? diff_row_token(g, r) : 0, hq = hk * g.group + (live ? r - t * g.group : 0);
-  const long long token = live ? s.token(t) : 0;
+  const DiffRow q = diff_query_row(g, s, box, r6);
+  const bool live = q.live;
+  const int hq = hk * g.group + (live ? q.head : 0), token = live ? s.token(q.x, q.y) : 0;
   const float lam = diff_lambda<F16>(a.lam, g.lam_f32, hq);
   float d1 = 0.f, d2 = 0.f;
   if (live && lane * 8 < g.dv) {
-    const long long at = s.b * g.o.b + token * g.o.t + hq * g.o.h + lane * 8;
+    const long long at = s.b * g.o.b + wide(token, g.o.t) + wide(hq, g.o.h) + lane * 8;
     const uint4 dw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.dO) + at);
     const uint4 ow = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o) + at);
     const uint4 pw = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.o2) + at);
@@ -92,13 +123,13 @@ __global__ void __launch_bounds__(256) diff_attn_rows_kernel(const DiffBwdArgs a
       const float v = a.lse[((static_cast<long long>(m) * g.batch + s.b) * g.q_heads + hq) * g.q_len + token];
       l[m] = v == -INFINITY ? -INFINITY : fmaf(-kDiffLog2e, v, kShift<F16>);
     }
-  float* w = a.rows + static_cast<long long>(unit) * a.rows_pad + r;
-  w[kRowL1 * a.row_stride] = l[0];
-  w[kRowL2 * a.row_stride] = l[1];
-  w[kRowD1 * a.row_stride] = -d1;
-  w[kRowD2 * a.row_stride] = -d2;
-  w[kRowLam * a.row_stride] = live ? -lam : 0.f;
-  w[kRowSeen * a.row_stride] = __int_as_float(live ? diff_visible(g, s, t) : 0);
+  float* w = a.rows + box_at * (kRowArrays * 64) + r6;
+  w[kRowL1 * 64] = l[0];
+  w[kRowL2 * 64] = l[1];
+  w[kRowD1 * 64] = -d1;
+  w[kRowD2 * 64] = -d2;
+  w[kRowLam * 64] = live ? -lam : 0.f;
+  w[kRowSum * 64] = 0.f;
 }
 
 // ------------------------------------------------------------------- dQ kernel
@@ -112,16 +143,21 @@ struct DqLay {
   static constexpr int STAGE = 2 * TK::BYTES + TV::BYTES;
   static constexpr int NS = 4;
   static constexpr int OFF_ST = OWN;
-  static constexpr int OFF_BAR = OFF_ST + NS * STAGE;
-  static constexpr int NBAR = 1 + 2 * NS + 6 + 1;   // own, st_full, st_empty, s_full[2], x_full[2], x_done[2], done
+  static constexpr int OFF_SUM = OFF_ST + NS * STAGE;  // [4][128] fp32: sums of P_2 dP
+  static constexpr int OFF_BAR = OFF_SUM + 4 * 128 * 4;
+  static constexpr int NBAR = 1 + 3 * NS + 6 + 1;      // own, st_full, st_empty, raw, s_full[2], x_full[2], x_done[2], done
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  // two buffers of S_1, S_2, dP (64 columns each); dS_i overwrites S_i's first 32
+  // two buffers of S_1, S_2, dP (64 columns each); dS_i overwrites the first
+  // half of each 32 columns of S_i
   static constexpr uint32_t BUF = 192, Q1 = 384, Q2 = 448, COLS = 512;
 };
 
-template <int D, int DV, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwdArgs a, int q_tiles) {
+template <int D, int DV, bool F16, int POLY>
+__global__ void __launch_bounds__(kThreads, 1)
+diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
+                    const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k1,
+                    const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_v, const DiffBwdArgs a, int q_tiles) {
   using Lay = DqLay<D, DV>;
   using TQ = typename Lay::TQ;
   using TO = typename Lay::TO;
@@ -133,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
   uint64_t* own = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* st_full = own + 1;
   uint64_t* st_empty = st_full + NS;
-  uint64_t* s_full = st_empty + NS;
+  uint64_t* raw = st_empty + NS;
+  uint64_t* s_full = raw + NS;
   uint64_t* x_full = s_full + 2;
   uint64_t* x_done = s_full + 4;
   uint64_t* done = s_full + 6;
@@ -147,21 +184,23 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
   u /= q_tiles;
   const int unit = u, hk = u % g.kv_heads;
   const DiffSeq s = diff_sequence(g, u / g.kv_heads);
-  const int rows = s.nq * g.group, row0 = qt * kOwn;
-  if (row0 >= rows) return;
-  const int most = diff_visible(g, s, diff_row_token(g, min(row0 + kOwn, rows) - 1));
-  const int least = diff_visible(g, s, diff_row_token(g, row0));   // the keys that every row of the tile sees
-  const int n = (most + kStream - 1) / kStream;
+  const int q_boxes = diff_q_boxes(g, s);
+  if (2 * qt >= q_boxes) return;
+  const int k_nx = g.causal ? ceil_div(diff_visible(g, s, min((2 * qt + 2) * g.tcq, s.wq) - 1), g.tck) : ceil_div(s.wk, g.tck);
+  const int n = k_nx * ceil_div(s.hk, g.trk);
+  const bool cut = s.wk % g.tck || s.hk % g.trk;
+  const bool clear = cut && (g.window || g.k_lens);
 
   if (threadIdx.x == 0) {
-    mbar_init(own, kLoadWarps);
+    mbar_init(own, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&st_full[i], kLoadWarps);
+      mbar_init(&st_full[i], 1);
+      mbar_init(&raw[i], 1);
       mbar_init(&st_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&s_full[i], 1);
-      mbar_init(&x_full[i], 4);
+      mbar_init(&x_full[i], 8);
       mbar_init(&x_done[i], 1);
     }
     mbar_init(done, 2);
@@ -169,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
     tmem_holder[2] = 0u;
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == kWarpS) {
     tmem_alloc(tmem_holder, Lay::COLS);
     tmem_relinquish();
   }
@@ -181,174 +220,194 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dq_kernel(const DiffBwd
   const WaitCtx drain{tmem_holder + 2, a.err};
   const uint32_t so = smem_u32(smem), sst = so + Lay::OFF_ST;
 
-  if (warp >= 10) {
-    // ------------------------------------------------------------ loaders
-    const int tid = threadIdx.x - 10 * 32;
-    const long long qb = s.b * g.q.b + static_cast<long long>(hk) * g.group * g.q.h;
-    const long long ob = s.b * g.o.b + static_cast<long long>(hk) * g.group * g.o.h;
-    const long long kb = s.b * g.k.b + hk * g.k.h;
-    const uint16_t* k1 = static_cast<const uint16_t*>(a.k1) + kb;
-    const uint16_t* k2 = static_cast<const uint16_t*>(a.k2) + kb;
-    const uint16_t* v = static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h;
-    int told = -1;   // -1: nothing handed over, 0: the own tiles, i + 1: key tile i
-    auto tell = [&](int upto) {
-      if (upto <= told) return;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int i = told + 1; i <= upto; ++i) mbar_arrive(i == 0 ? own : &st_full[(i - 1) % NS]);
-      told = upto;
-    };
-    if (n > 0) {
-      diff_clear<D, DV, kLoaders>(smem, Lay::OFF_BAR, g, tid);
-      diff_load_queries<kOwn, D, DV, kLoaders>(so, static_cast<const uint16_t*>(a.q1) + qb, static_cast<const uint16_t*>(a.q2) + qb,
-                                               static_cast<const uint16_t*>(a.dO) + ob, g, s, row0, rows, tid);
-      cp_async_commit();
-    }
-    for (int i = 0; i < n; ++i) {
-      const int st = i % NS;
-      if (i >= NS) {
-        const uint32_t parity = ((i / NS) - 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(&st_empty[st], parity))) {
-          cp_async_wait<0>();
-          tell(i);
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st_empty[st], parity, wc, SITE_ST_EMPTY))) break;
+  if (warp == kWarpLoad) {
+    // --------------------------------------------------------- TMA producer
+    if (lane == 0 && n > 0) {
+      const int nx_q = ceil_div(s.wq, g.tcq), halves = min(2, q_boxes - 2 * qt), q_rows = g.tcq * g.trq * g.group;
+      mbar_arrive_expect_tx(own, halves * (2 * TQ::box_bytes(q_rows) + TO::box_bytes(q_rows)));
+      for (int h = 0; h < halves; ++h) {
+        const int box = 2 * qt + h, by = box / nx_q, x = s.x0 + (box - by * nx_q) * g.tcq, y = s.y0 + by * g.trq;
+        TQ::load(smem, h, &tm_q1, own, hk * g.group, x, y, s.b);
+        TQ::load(smem + TQ::BYTES, h, &tm_q2, own, hk * g.group, x, y, s.b);
+        TO::load(smem + 2 * TQ::BYTES, h, &tm_do, own, hk * g.group, x, y, s.b);
+      }
+      const uint32_t bytes = 2 * TK::box_bytes(kStream) + TV::box_bytes(kStream);
+      int bx = 0, by = 0, issued = 0;
+      uint64_t* to_full = clear ? raw : st_full;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (i >= NS && !mbar_wait(&st_empty[st], ((i / NS) - 1) & 1, wc, SITE_ST_EMPTY)) break;
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        const int x = s.x0 + bx * g.tck, y = s.y0 + by * g.trk;
+        mbar_arrive_expect_tx(&to_full[st], bytes);
+        TK::load(to, 0, &tm_k1, &to_full[st], hk, x, y, s.b);
+        TK::load(to + TK::BYTES, 0, &tm_k2, &to_full[st], hk, x, y, s.b);
+        TV::load(to + 2 * TK::BYTES, 0, &tm_v, &to_full[st], hk, x, y, s.b);
+        issued = i + 1;
+        if (++bx == k_nx) {
+          bx = 0;
+          ++by;
         }
       }
-      const uint32_t b = sst + st * Lay::STAGE;
-      diff_load_keys<kStream, D, DV, kLoaders>(b, k1, k2, v, g, s, i * kStream, s.nk, tid);
-      cp_async_commit();
-      cp_async_wait<1>();
-      tell(i);
+      mbar_wait(own, 0, drain, SITE_DONE);
+      for (int i = max(0, issued - NS); i < issued; ++i) mbar_wait(&to_full[i % NS], (i / NS) & 1, drain, SITE_DONE);
     }
-    cp_async_wait<0>();
-    if (n > 0 && *abort_flag == 0u) tell(n);
-  } else if (warp == 8 || warp == 9) {
-    // two MMA issuers: warp 8 the scores and dP, warp 9 the gradients
-    if (lane == 0 && n > 0) {
+  } else if (warp == kWarpClear) {
+    if (clear)
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (!warp_wait(&raw[st], (i / NS) & 1, wc, SITE_RAW)) break;
+        const DiffKeyBox k = diff_key_box(g, s, k_nx, i);
+        const uint64_t mask = diff_key_mask(g, k.vx, k.vy);
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        if (mask != ~0ull) {
+          for (int row = 0; row < kStream; ++row)
+            if (!((mask >> row) & 1ull)) {
+              TK::clear_row(to, row, lane, 32);
+              TK::clear_row(to + TK::BYTES, row, lane, 32);
+              TV::clear_row(to + 2 * TK::BYTES, row, lane, 32);
+            }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[st]);
+      }
+  } else if (warp == kWarpS || warp == kWarpX) {
+    // two MMA issuers: the scores and dP, and the gradients
+    if (n > 0) {
       const uint32_t id_s = diff_idesc(F16, kStream, false);
       const uint32_t id_q = diff_idesc(F16, (g.d + 15) / 16 * 16, true);
-      const int ks_d = (g.d + 15) / 16, ks_v = (g.dv + 15) / 16;
-      bool ok = mbar_wait(own, 0, wc, SITE_OWN);
+      const uint64_t q1 = TQ::kmajor(so), q2 = TQ::kmajor(so + TQ::BYTES), dO = TO::kmajor(so + 2 * TQ::BYTES);
+      const uint64_t kk = TK::kmajor(sst), kv = TV::kmajor(sst + 2 * TK::BYTES), km = TK::mnmajor(sst);
+      bool ok = warp_wait(own, 0, wc, SITE_OWN);
+      int st = 0;
+      uint32_t lap = 0;
       for (int j = 0; ok && j < n; ++j) {
-        const int st = j % NS, bb = j & 1;
-        const uint32_t b = sst + st * Lay::STAGE, t = tmem + Lay::BUF * bb;
-        if (warp == 8) {
-          if (!(ok = mbar_wait(&st_full[st], (j / NS) & 1, wc, SITE_ST_FULL))) break;
-          if (j >= 2 && !(ok = mbar_wait(&x_done[bb], ((j - 2) >> 1) & 1, wc, SITE_X_DONE))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            if (ks < ks_d) umma_ss(t, TQ::kmajor(so, ks), TK::kmajor(b, ks), id_s, ks > 0 ? 1u : 0u);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            if (ks < ks_d) umma_ss(t + 64, TQ::kmajor(so + TQ::BYTES, ks), TK::kmajor(b + TK::BYTES, ks), id_s, ks > 0 ? 1u : 0u);
-#pragma unroll
-          for (int ks = 0; ks < DV / 16; ++ks)
-            if (ks < ks_v)
-              umma_ss(t + 128, TO::kmajor(so + 2 * TQ::BYTES, ks), TV::kmajor(b + 2 * TK::BYTES, ks), id_s, ks > 0 ? 1u : 0u);
-          umma_commit(&s_full[bb]);
+        const int bb = j & 1;
+        const uint32_t at = static_cast<uint32_t>(st) * (Lay::STAGE >> 4), t = tmem + Lay::BUF * bb;
+        if (warp == kWarpS) {
+          ok = warp_wait(&st_full[st], lap, wc, SITE_ST_FULL);
+          if (ok && j >= 2) ok = warp_wait(&x_done[bb], ((j - 2) >> 1) & 1, wc, SITE_X_DONE);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            diff_mma_kk<TQ, TK, D / 16>(t, q1, kk + at, id_s);
+            diff_mma_kk<TQ, TK, D / 16>(t + 64, q2, kk + at + (TK::BYTES >> 4), id_s);
+            diff_mma_kk<TO, TV, DV / 16>(t + 128, dO, kv + at, id_s);
+            umma_commit(&s_full[bb]);
+            umma_commit(&st_empty[st]);
+          }
         } else {
-          if (!(ok = mbar_wait(&x_full[bb], (j >> 1) & 1, wc, SITE_X_FULL))) break;
-          tc_fence_after();
+          ok = warp_wait(&x_full[bb], (j >> 1) & 1, wc, SITE_X_FULL);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint32_t acc = j > 0 ? 1u : 0u;
 #pragma unroll
-          for (int ks = 0; ks < kStream / 16; ++ks)
-            umma_ts(tmem + Lay::Q1, t + 8u * ks, TK::mnmajor(b, ks), id_q, (j > 0 || ks > 0) ? 1u : 0u);
+            for (int ks = 0; ks < kStream / 16; ++ks)
+              umma_ts(tmem + Lay::Q1, t + 32u * (ks >> 1) + 8u * (ks & 1), km + at + TK::mnstep(ks), id_q, ks > 0 ? 1u : acc);
 #pragma unroll
-          for (int ks = 0; ks < kStream / 16; ++ks)
-            umma_ts(tmem + Lay::Q2, t + 64 + 8u * ks, TK::mnmajor(b + TK::BYTES, ks), id_q, (j > 0 || ks > 0) ? 1u : 0u);
-          umma_commit(&x_done[bb]);
+            for (int ks = 0; ks < kStream / 16; ++ks)
+              umma_ts(tmem + Lay::Q2, t + 64 + 32u * (ks >> 1) + 8u * (ks & 1), km + at + (TK::BYTES >> 4) + TK::mnstep(ks), id_q,
+                      ks > 0 ? 1u : acc);
+            umma_commit(&x_done[bb]);
+            umma_commit(&st_empty[st]);
+          }
         }
-        umma_commit(&st_empty[st]);
+        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          lap ^= 1u;
+        }
       }
-      umma_commit(done);
-      mbar_wait(done, 0, drain, SITE_DONE);
+      if (elect_one()) umma_commit(done);
+      warp_wait(done, 0, drain, SITE_DONE);
     }
   } else {
-    // elementwise: warpgroup w takes the tiles j = w, w + 2, ...; thread = query row = TMEM lane
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane, r = row0 + row;
+    // elementwise: warpgroup (p, h) takes columns 32 h .. of the tiles j = p, p + 2, ...; thread = query row
+    const int w = warp >> 2, p = w >> 1, h = w & 1, row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t = tmem + lane_off + Lay::BUF * w;
-    const float* c = a.rows + static_cast<long long>(unit) * a.rows_pad + r;
-    const float l1 = c[kRowL1 * a.row_stride], l2 = c[kRowL2 * a.row_stride], d1 = c[kRowD1 * a.row_stride], d2 = c[kRowD2 * a.row_stride];
-    const float nlam = c[kRowLam * a.row_stride];
-    const int seen = __float_as_int(c[kRowSeen * a.row_stride]);
-    const bool warp_live = row0 + (warp & 3) * 32 < rows;
+    const uint32_t t = tmem + lane_off + Lay::BUF * p + 32 * h;
+    const DiffRow q = diff_query_row(g, s, 2 * qt + (row >> 6), row & 63);
+    float* c = a.rows + ((static_cast<long long>(unit) * a.boxes + 2 * qt + (row >> 6)) * kRowArrays) * 64 + (row & 63);
+    const float l1 = c[kRowL1 * 64], l2 = c[kRowL2 * 64], d1 = c[kRowD1 * 64], d2 = c[kRowD2 * 64], nlam = c[kRowLam * 64];
+    const int seen = q.live ? diff_visible(g, s, q.x) : 0x7FFFFFFF;
+    const bool warp_live = __any_sync(0xFFFFFFFFu, q.live);
     const uint64_t sl2 = f2_pack(g.scale_log2, g.scale_log2), L1 = f2_pack(l1, l1), L2 = f2_pack(l2, l2), D1 = f2_pack(d1, d1), D2 = f2_pack(d2, d2);
     const uint64_t NL = f2_pack(nlam, nlam);
+    uint64_t sum = f2_pack(0.f, 0.f);   // of P_2 dP
     bool ok = true;
-    for (int j = w; j < n; j += 2) {
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[w], (j >> 1) & 1, wc, SITE_S_FULL));
+    for (int j = p; j < n; j += 2) {
+      ok = warp_wait(&s_full[p], (j >> 1) & 1, wc, SITE_S_FULL);
       if (!ok) break;
       tc_fence_after();
       if (warp_live) {
-        const bool edge = (j + 1) * kStream > least;
+        uint32_t hidden = 0u;   // a bit for every column that the row does not see
+        if (cut || g.causal) {
+          const uint64_t mask = diff_seen(g, s, k_nx, j, seen);
+          hidden = ~static_cast<uint32_t>(mask >> (32 * h));
+        }
+        const bool edge = __any_sync(0xFFFFFFFFu, hidden != 0u);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t s1[32], s2[32], dp[32], x1[16], x2[16];
-          tmem_ld32(t + 32 * h, s1);
-          tmem_ld32(t + 64 + 32 * h, s2);
-          tmem_ld32(t + 128 + 32 * h, dp);
+        for (int cc = 0; cc < 2; ++cc) {
+          uint32_t s1[16], s2[16], dp[16], x1[8], x2[8];
+          tmem_ld16(t + 16 * cc, s1);
+          tmem_ld16(t + 64 + 16 * cc, s2);
+          tmem_ld16(t + 128 + 16 * cc, dp);
           tmem_wait_ld();
           if (edge) {
-            const int left = seen - j * kStream - 32 * h;
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= left) s1[i] = s2[i] = 0xFF800000u;   // -inf: P = 0
+            for (int i = 0; i < 16; ++i)
+              if (hidden & (1u << (16 * cc + i))) s1[i] = s2[i] = 0xFF800000u;   // -inf: P = 0
           }
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(s1[2 * i]), __uint_as_float(s1[2 * i + 1])), sl2, L1);
-            const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(s2[2 * i]), __uint_as_float(s2[2 * i + 1])), sl2, L2);
-            const uint64_t dd = f2_pack(__uint_as_float(dp[2 * i]), __uint_as_float(dp[2 * i + 1]));
-            float a0, a1, b0, b1;
-            f2_unpack(y1, a0, a1);
-            f2_unpack(y2, b0, b1);
-            const uint64_t e1 = f2_mul(f2_pack(ex2_approx(a0), ex2_approx(a1)), f2_add(dd, D1));
-            const uint64_t e2 = f2_mul(f2_mul(f2_pack(ex2_approx(b0), ex2_approx(b1)), NL), f2_add(dd, D2));
-            f2_unpack(e1, a0, a1);
-            f2_unpack(e2, b0, b1);
-            x1[i] = diff_pack<F16>(a0, a1);
-            x2[i] = diff_pack<F16>(b0, b1);
+          for (int i = 0; i < 8; ++i) {
+            const uint64_t dd = raw_pair(dp + 2 * i);
+            const uint64_t y1 = f2_fma(raw_pair(s1 + 2 * i), sl2, L1), y2 = f2_fma(raw_pair(s2 + 2 * i), sl2, L2);
+            const bool poly = i < POLY;
+            const uint64_t p1 = poly ? exp2_pair<true>(y1) : exp2_pair<false>(y1);
+            const uint64_t p2 = poly ? exp2_pair<true>(y2) : exp2_pair<false>(y2);
+            sum = f2_fma(p2, dd, sum);
+            x1[i] = pack_pair<F16>(f2_mul(p1, f2_add(dd, D1)));
+            x2[i] = pack_pair<F16>(f2_mul(f2_mul(p2, NL), f2_add(dd, D2)));
           }
-          tmem_st16(t + 16 * h, x1);
-          tmem_st16(t + 64 + 16 * h, x2);
+          tmem_st8(t + 8 * cc, x1);
+          tmem_st8(t + 64 + 8 * cc, x2);
         }
         tmem_wait_st();
       }
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&x_full[w]);
+      if (lane == 0) mbar_arrive(&x_full[p]);
     }
-    if (ok && n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(done, 0, wc, SITE_DONE));
+    float* sums = reinterpret_cast<float*>(smem + Lay::OFF_SUM);
+    float s0, s1;
+    f2_unpack(sum, s0, s1);
+    sums[w * 128 + row] = s0 + s1;
+    if (ok && n > 0) ok = warp_wait(done, 0, wc, SITE_DONE);
+    asm volatile("bar.sync 1, 512;" ::: "memory");
     tc_fence_after();
     if (ok && warp_live && *abort_flag == 0u) {
-      // warpgroup w stores dQ_(w + 1); without a key in sight the gradient is zero
-      const float f = n > 0 ? g.scale * kUnshift<F16> : 0.f;
-      const bool live = r < rows;
-      const int tk = diff_row_token(g, r);
-      uint16_t* out = static_cast<uint16_t*>(w ? a.dq2 : a.dq1);
-      if (live) out += s.b * g.q.b + s.token(tk) * g.q.t + (hk * g.group + r - tk * g.group) * g.q.h;
+      if (w == 0 && q.live)
+        c[kRowSum * 64] = -kUnshift<F16> * ((sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]));
+      // warpgroup (p, h) stores columns h D / 2 .. of dQ_(p + 1); without a key in sight the gradient is zero
+      const float f = g.scale * kUnshift<F16>;
+      uint16_t* out = static_cast<uint16_t*>(p ? a.dq2 : a.dq1);
+      if (q.live) out += s.b * g.q.b + wide(s.token(q.x, q.y), g.q.t) + wide(hk * g.group + q.head, g.q.h);
 #pragma unroll
       for (int cc = 0; cc < D / 16; ++cc) {
-        uint32_t v[16];
-        tmem_ld16(tmem + lane_off + (w ? Lay::Q2 : Lay::Q1) + 16 * cc, v);
+        const int col = h * (D / 2) + 8 * cc;
+        uint32_t v[8], o[4];
+        tmem_ld8(tmem + lane_off + (p ? Lay::Q2 : Lay::Q1) + col, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) v[i] = n > 0 ? __float_as_uint(__uint_as_float(v[i]) * f) : 0u;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t o[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] = diff_pack<F16>(__uint_as_float(v[8 * h + 2 * e]), __uint_as_float(v[8 * h + 2 * e + 1]));
-          if (live && 16 * cc + 8 * h < g.d) *reinterpret_cast<uint4*>(out + 16 * cc + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
-        }
+        for (int e = 0; e < 4; ++e)
+          o[e] = n > 0 ? diff_pack<F16>(__uint_as_float(v[2 * e]) * f, __uint_as_float(v[2 * e + 1]) * f) : 0u;
+        if (q.live && col < g.d) *reinterpret_cast<uint4*>(out + col) = make_uint4(o[0], o[1], o[2], o[3]);
       }
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kWarpS) {
     tc_fence_after();
     tmem_dealloc(tmem, Lay::COLS);
   }
@@ -362,29 +421,40 @@ struct DkvLay {
   using TQ = DiffTile<kStream, D>;
   using TO = DiffTile<kStream, DV>;
   using TP = DiffTile<kOwn, kStream>;      // P^T, dS_1^T, dS_2^T: [128 keys][64 query rows]
+  // Buffers of the scores and of P^T, dS^T. Two where TMEM holds them (dv <=
+  // 64): tiles alternate between two pairs of warpgroups. One at dv = 128: the
+  // four warpgroups share a tile and free S as soon as it is in registers.
+  static constexpr int NB = DV <= 64 ? 2 : 1;
+  static constexpr int PER = 16 * NB;      // query rows of a warpgroup's share
   static constexpr int OWN = 2 * TK::BYTES + TV::BYTES;
   static constexpr int CONSTS = kRowArrays * kStream * 4;
   static constexpr int STAGE = (2 * TQ::BYTES + TO::BYTES + CONSTS + 1023) / 1024 * 1024;
-  static constexpr int NS = STAGE <= 16 * 1024 ? 4 : 3;
+  static constexpr int NS = DV <= 64 ? 4 : 3;
   static constexpr int OFF_ST = OWN;
   static constexpr int OFF_X = OFF_ST + NS * STAGE;
-  static constexpr int OFF_BAR = OFF_X + 3 * TP::BYTES;
-  static constexpr int NBAR = 1 + 2 * NS + 4 + 1;   // own, st_full, st_empty, s_full, s_free, x_full, x_free, done
+  static constexpr int X = 3 * TP::BYTES;
+  static constexpr int OFF_BAR = OFF_X + NB * X;
+  static constexpr int NBAR = 1 + 3 * NS + 8 + 1;   // own, st_full, st_empty, raw, s_full[2], s_free[2], x_full[2], x_free[2], done
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory of an SM");
-  static constexpr uint32_t S1 = 0, S2 = 64, DP = 128, V = 192, K1 = V + DV, K2 = K1 + D, COLS = K2 + D <= 256 ? 256 : 512;
+  static constexpr uint32_t BUF = 192, S2 = 64, DP = 128, V = BUF * NB, K1 = V + DV, K2 = K1 + D, COLS = 512;
+  static_assert(K2 + D <= 512, "TMEM columns");
 };
 
-template <int D, int DV, bool F16>
-__global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBwdArgs a, int k_tiles, int units) {
+template <int D, int DV, bool F16, int POLY>
+__global__ void __launch_bounds__(kThreads, 1)
+diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
+                     const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k1,
+                     const __grid_constant__ CUtensorMap tm_k2, const __grid_constant__ CUtensorMap tm_v, const DiffBwdArgs a, int k_tiles,
+                     int units) {
   using Lay = DkvLay<D, DV>;
   using TQ = typename Lay::TQ;
   using TO = typename Lay::TO;
   using TK = typename Lay::TK;
   using TV = typename Lay::TV;
   using TP = typename Lay::TP;
-  constexpr int NS = Lay::NS;
+  constexpr int NS = Lay::NS, NB = Lay::NB;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   const DiffGeom& g = a.g;
@@ -392,14 +462,17 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
 
   int u = blockIdx.x / k_tiles;
   if (u >= units) {
-    // dlambda of one head: its rows' -D_2 over every sequence, each thread a
+    // dlambda of one head: its rows' sums over every sequence, each thread a
     // strided share, then a tree
-    const int h = blockIdx.x - units * k_tiles, hk = h / g.group;
+    const int hq = blockIdx.x - units * k_tiles, hk = hq / g.group, gh = hq - hk * g.group;
+    const int per = g.tcq * g.trq;
+    const long long total = static_cast<long long>(units / g.kv_heads) * a.boxes * per;
     float sum = 0.f;
-    const long long per = a.rows_pad / g.group, total = static_cast<long long>(units / g.kv_heads) * per;
     for (long long i = threadIdx.x; i < total; i += kThreads) {
-      const long long q = i / per, t = i - q * per;
-      sum += a.rows[kRowD2 * a.row_stride + (q * g.kv_heads + hk) * a.rows_pad + t * g.group + (h - hk * g.group)];
+      const long long box = i / per;
+      const int idx = static_cast<int>(i - box * per);
+      const long long seq = box / a.boxes;
+      sum += a.rows[(((seq * g.kv_heads + hk) * a.boxes + (box - seq * a.boxes)) * kRowArrays + kRowSum) * 64 + idx * g.group + gh];
     }
     float* red = reinterpret_cast<float*>(smem);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -408,54 +481,67 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
     if (threadIdx.x == 0) {
       float v = 0.f;
       for (int i = 0; i < kThreads / 32; ++i) v += red[i];
-      if (g.lam_f32) static_cast<float*>(a.dlam)[h] = v;
-      else static_cast<uint16_t*>(a.dlam)[h] = static_cast<uint16_t>(diff_pack<F16>(v, 0.f));
+      if (g.lam_f32) static_cast<float*>(a.dlam)[hq] = v;
+      else static_cast<uint16_t*>(a.dlam)[hq] = static_cast<uint16_t>(diff_pack<F16>(v, 0.f));
     }
     return;
   }
   uint64_t* own = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* st_full = own + 1;
   uint64_t* st_empty = st_full + NS;
-  uint64_t* s_full = st_empty + NS;
-  uint64_t* s_free = s_full + 1;
-  uint64_t* x_full = s_full + 2;
-  uint64_t* x_free = s_full + 3;
-  uint64_t* done = s_full + 4;
+  uint64_t* raw = st_empty + NS;
+  uint64_t* s_full = raw + NS;
+  uint64_t* s_free = s_full + 2;
+  uint64_t* x_full = s_full + 4;
+  uint64_t* x_free = s_full + 6;
+  uint64_t* done = s_full + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile uint32_t* abort_flag = tmem_holder + 1;
-  const int key0 = (blockIdx.x - u * k_tiles) * kOwn;   // with a causal mask the first keys have the most rows
+  const int kt = blockIdx.x - u * k_tiles;              // with a causal mask the first keys have the most rows
   const int unit = u, hk = u % g.kv_heads;
   const DiffSeq s = diff_sequence(g, u / g.kv_heads);
-  const int all = g.window ? s.nk : g.k_len;            // keys whose gradients are written
-  if (key0 >= all) return;
-  const int rows = s.nq * g.group;
-  // the first row that sees key0, and the first from which every row sees the whole tile
+  const int all = g.window ? s.wk : g.k_len;            // keys whose gradients are written
+  const int k_nx = ceil_div(all, g.tck), k_boxes = k_nx * ceil_div(s.hk, g.trk);
+  if (2 * kt >= k_boxes) return;
+  const int q_nx = ceil_div(s.wq, g.tcq), q_boxes = diff_q_boxes(g, s);
+  // sequences: the first row that sees one of the keys, and the first from which every row sees them all
+  const int key0 = kt * kOwn;
   int first = 0, full = 0;
   if (g.causal) {
-    first = min(max(key0 - s.nk + s.nq, 0), s.nq) * g.group;
-    full = min(max(min(key0 + kOwn, s.nk) - 1 - s.nk + s.nq, 0), s.nq) * g.group;
+    first = min(max(key0 - s.wk + s.wq, 0), s.wq);
+    full = min(max(min(key0 + kOwn, s.wk) - 1 - s.wk + s.wq, 0), s.wq);
   }
-  if (key0 >= s.nk) first = rows;
-  const int j0 = first / kStream, n = first < rows ? (rows + kStream - 1) / kStream - j0 : 0;
+  const int j0 = first / g.tcq * (g.causal ? 1 : 0), n = !g.window && (key0 >= s.wk || first >= s.wq) ? 0 : q_boxes - j0;
+  const int q_rows = g.tcq * g.trq * g.group;
+  const bool clear = g.window && (s.wq % g.tcq || s.hq % g.trq);   // boxes with another window's rows
 
   if (threadIdx.x == 0) {
-    mbar_init(own, kLoadWarps);
+    mbar_init(own, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&st_full[i], kLoadWarps);
+      mbar_init(&st_full[i], 1);
+      mbar_init(&raw[i], 1);
       mbar_init(&st_empty[i], 2);
     }
-    mbar_init(s_full, 1);
-    mbar_init(s_free, 8);
-    mbar_init(x_full, 8);
-    mbar_init(x_free, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&s_full[i], 1);
+      mbar_init(&s_free[i], 16 / NB);
+      mbar_init(&x_full[i], 16 / NB);
+      mbar_init(&x_free[i], 1);
+    }
     mbar_init(done, 2);
     tmem_holder[1] = 0u;
     tmem_holder[2] = 0u;
     fence_barrier_init();
   }
-  if (warp == 8) {
+  if (warp == kWarpS) {
     tmem_alloc(tmem_holder, Lay::COLS);
     tmem_relinquish();
+  }
+  if (q_rows < 64) {
+    // rows of a stage that no load writes are zeros
+    for (int i = Lay::OFF_ST + threadIdx.x * 16; i < Lay::OFF_X; i += kThreads * 16)
+      *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
   }
   tc_fence_before();
   __syncthreads();
@@ -465,193 +551,220 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
   const WaitCtx drain{tmem_holder + 2, a.err};
   const uint32_t so = smem_u32(smem), sst = so + Lay::OFF_ST, sx = so + Lay::OFF_X;
 
-  if (warp >= 10) {
-    // ------------------------------------------------------------ loaders
-    const int tid = threadIdx.x - 10 * 32;
-    const long long qb = s.b * g.q.b + static_cast<long long>(hk) * g.group * g.q.h;
-    const long long kb = s.b * g.k.b + hk * g.k.h;
-    const uint16_t* q1 = static_cast<const uint16_t*>(a.q1) + qb;
-    const uint16_t* q2 = static_cast<const uint16_t*>(a.q2) + qb;
-    const uint16_t* dO = static_cast<const uint16_t*>(a.dO) + s.b * g.o.b + static_cast<long long>(hk) * g.group * g.o.h;
-    const float* consts = a.rows + static_cast<long long>(unit) * a.rows_pad;
-    int told = -1;
-    auto tell = [&](int upto) {
-      if (upto <= told) return;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int i = told + 1; i <= upto; ++i) mbar_arrive(i == 0 ? own : &st_full[(i - 1) % NS]);
-      told = upto;
-    };
-    if (n > 0) {
-      diff_clear<D, DV, kLoaders>(smem, Lay::OFF_X, g, tid);
-      diff_load_keys<kOwn, D, DV, kLoaders>(so, static_cast<const uint16_t*>(a.k1) + kb, static_cast<const uint16_t*>(a.k2) + kb,
-                                            static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h, g, s, key0, s.nk, tid);
-      cp_async_commit();
-    }
-    for (int i = 0; i < n; ++i) {
-      const int st = i % NS;
-      if (i >= NS) {
-        const uint32_t parity = ((i / NS) - 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(&st_empty[st], parity))) {
-          cp_async_wait<0>();
-          tell(i);
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&st_empty[st], parity, wc, SITE_ST_EMPTY))) break;
+  if (warp == kWarpLoad) {
+    // --------------------------------------------------------- TMA producer
+    if (lane == 0 && n > 0) {
+      const int halves = min(2, k_boxes - 2 * kt);
+      mbar_arrive_expect_tx(own, halves * (2 * TK::box_bytes(64) + TV::box_bytes(64)));
+      for (int h = 0; h < halves; ++h) {
+        const int box = 2 * kt + h, by = box / k_nx, x = s.x0 + (box - by * k_nx) * g.tck, y = s.y0 + by * g.trk;
+        TK::load(smem, h, &tm_k1, own, hk, x, y, s.b);
+        TK::load(smem + TK::BYTES, h, &tm_k2, own, hk, x, y, s.b);
+        TV::load(smem + 2 * TK::BYTES, h, &tm_v, own, hk, x, y, s.b);
+      }
+      const uint32_t bytes = 2 * TQ::box_bytes(q_rows) + TO::box_bytes(q_rows) + Lay::CONSTS;
+      const float* consts = a.rows + (static_cast<long long>(unit) * a.boxes + j0) * (kRowArrays * 64);
+      int by = j0 / q_nx, bx = j0 - by * q_nx, issued = 0;
+      uint64_t* to_full = clear ? raw : st_full;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (i >= NS && !mbar_wait(&st_empty[st], ((i / NS) - 1) & 1, wc, SITE_ST_EMPTY)) break;
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        const int x = s.x0 + bx * g.tcq, y = s.y0 + by * g.trq;
+        mbar_arrive_expect_tx(&to_full[st], bytes);
+        TQ::load(to, 0, &tm_q1, &to_full[st], hk * g.group, x, y, s.b);
+        TQ::load(to + TQ::BYTES, 0, &tm_q2, &to_full[st], hk * g.group, x, y, s.b);
+        TO::load(to + 2 * TQ::BYTES, 0, &tm_do, &to_full[st], hk * g.group, x, y, s.b);
+        bulk_load(to + 2 * TQ::BYTES + TO::BYTES, consts + static_cast<long long>(i) * (kRowArrays * 64), Lay::CONSTS, &to_full[st]);
+        issued = i + 1;
+        if (++bx == q_nx) {
+          bx = 0;
+          ++by;
         }
       }
-      const uint32_t b = sst + st * Lay::STAGE;
-      const int r0 = (j0 + i) * kStream;
-      diff_load_queries<kStream, D, DV, kLoaders>(b, q1, q2, dO, g, s, r0, rows, tid);
-      for (int c = tid; c < kRowArrays * kStream / 4; c += kLoaders)   // 16 pieces of 4 rows an array; rows_pad covers the last tile
-        cp_async_16(smem + (b - so) + 2 * TQ::BYTES + TO::BYTES + c * 16, consts + (c / 16) * a.row_stride + r0 + (c % 16) * 4);
-      cp_async_commit();
-      cp_async_wait<1>();
-      tell(i);
+      mbar_wait(own, 0, drain, SITE_DONE);
+      for (int i = max(0, issued - NS); i < issued; ++i) mbar_wait(&to_full[i % NS], (i / NS) & 1, drain, SITE_DONE);
     }
-    cp_async_wait<0>();
-    if (n > 0 && *abort_flag == 0u) tell(n);
-  } else if (warp == 8 || warp == 9) {
-    if (lane == 0 && n > 0) {
+  } else if (warp == kWarpClear) {
+    if (clear)
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (!warp_wait(&raw[st], (i / NS) & 1, wc, SITE_RAW)) break;
+        const int by = (j0 + i) / q_nx, vx = s.wq - (j0 + i - by * q_nx) * g.tcq, vy = s.hq - by * g.trq;
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        if (vx < g.tcq || vy < g.trq) {
+          for (int row = 0; row < q_rows; ++row)
+            if (!diff_query_row(g, s, j0 + i, row).live) {
+              TQ::clear_row(to, row, lane, 32);
+              TQ::clear_row(to + TQ::BYTES, row, lane, 32);
+              TO::clear_row(to + 2 * TQ::BYTES, row, lane, 32);
+            }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&st_full[st]);
+      }
+  } else if (warp == kWarpS || warp == kWarpX) {
+    if (n > 0) {
       const uint32_t id_s = diff_idesc(F16, kStream, false);
       const uint32_t id_k = diff_idesc(F16, (g.d + 15) / 16 * 16, true), id_v = diff_idesc(F16, (g.dv + 15) / 16 * 16, true);
-      const int ks_d = (g.d + 15) / 16, ks_v = (g.dv + 15) / 16;
-      bool ok = mbar_wait(own, 0, wc, SITE_OWN);
+      const uint64_t k1 = TK::kmajor(so), k2 = TK::kmajor(so + TK::BYTES), v = TV::kmajor(so + 2 * TK::BYTES), x = TP::kmajor(sx);
+      const uint64_t qk = TQ::kmajor(sst), dk = TO::kmajor(sst + 2 * TQ::BYTES), qm = TQ::mnmajor(sst), dm = TO::mnmajor(sst + 2 * TQ::BYTES);
+      bool ok = warp_wait(own, 0, wc, SITE_OWN);
+      int st = 0;
+      uint32_t lap = 0;
       for (int j = 0; ok && j < n; ++j) {
-        const int st = j % NS;
-        const uint32_t b = sst + st * Lay::STAGE;
-        if (warp == 8) {
-          if (!(ok = mbar_wait(&st_full[st], (j / NS) & 1, wc, SITE_ST_FULL))) break;
-          if (j >= 1 && !(ok = mbar_wait(s_free, (j - 1) & 1, wc, SITE_S_FREE))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            if (ks < ks_d) umma_ss(tmem + Lay::S1, TK::kmajor(so, ks), TQ::kmajor(b, ks), id_s, ks > 0 ? 1u : 0u);
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            if (ks < ks_d)
-              umma_ss(tmem + Lay::S2, TK::kmajor(so + TK::BYTES, ks), TQ::kmajor(b + TQ::BYTES, ks), id_s, ks > 0 ? 1u : 0u);
-#pragma unroll
-          for (int ks = 0; ks < DV / 16; ++ks)
-            if (ks < ks_v)
-              umma_ss(tmem + Lay::DP, TV::kmajor(so + 2 * TK::BYTES, ks), TO::kmajor(b + 2 * TQ::BYTES, ks), id_s, ks > 0 ? 1u : 0u);
-          umma_commit(s_full);
-        } else {
-          if (!(ok = mbar_wait(x_full, j & 1, wc, SITE_X_FULL))) break;
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 0; ks < kStream / 16; ++ks) {
-            const uint32_t acc = (j > 0 || ks > 0) ? 1u : 0u;
-            umma_ss(tmem + Lay::V, TP::kmajor(sx, ks), TO::mnmajor(b + 2 * TQ::BYTES, ks), id_v, acc);
-            umma_ss(tmem + Lay::K1, TP::kmajor(sx + TP::BYTES, ks), TQ::mnmajor(b, ks), id_k, acc);
-            umma_ss(tmem + Lay::K2, TP::kmajor(sx + 2 * TP::BYTES, ks), TQ::mnmajor(b + TQ::BYTES, ks), id_k, acc);
+        const int bb = NB == 2 ? j & 1 : 0, round = NB == 2 ? j >> 1 : j;
+        const uint32_t at = static_cast<uint32_t>(st) * (Lay::STAGE >> 4);
+        if (warp == kWarpS) {
+          const uint32_t t = tmem + Lay::BUF * bb;
+          ok = warp_wait(&st_full[st], lap, wc, SITE_ST_FULL);
+          if (ok && round >= 1) ok = warp_wait(&s_free[bb], (round - 1) & 1, wc, SITE_S_FREE);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            diff_mma_kk<TK, TQ, D / 16>(t, k1, qk + at, id_s);
+            diff_mma_kk<TK, TQ, D / 16>(t + Lay::S2, k2, qk + at + (TQ::BYTES >> 4), id_s);
+            diff_mma_kk<TV, TO, DV / 16>(t + Lay::DP, v, dk + at, id_s);
+            umma_commit(&s_full[bb]);
+            umma_commit(&st_empty[st]);
           }
-          umma_commit(x_free);
+        } else {
+          ok = warp_wait(&x_full[bb], round & 1, wc, SITE_X_FULL);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint64_t xb = x + static_cast<uint32_t>(bb) * (Lay::X >> 4);
+            const uint32_t acc0 = j > 0 ? 1u : 0u;
+#pragma unroll
+            for (int ks = 0; ks < kStream / 16; ++ks) {
+              const uint32_t acc = ks > 0 ? 1u : acc0;
+              umma_ss(tmem + Lay::V, xb + TP::kstep(ks), dm + at + TO::mnstep(ks), id_v, acc);
+              umma_ss(tmem + Lay::K1, xb + (TP::BYTES >> 4) + TP::kstep(ks), qm + at + TQ::mnstep(ks), id_k, acc);
+              umma_ss(tmem + Lay::K2, xb + 2 * (TP::BYTES >> 4) + TP::kstep(ks), qm + at + (TQ::BYTES >> 4) + TQ::mnstep(ks), id_k, acc);
+            }
+            umma_commit(&x_free[bb]);
+            umma_commit(&st_empty[st]);
+          }
         }
-        umma_commit(&st_empty[st]);
+        __syncwarp();
+        if (++st == NS) {
+          st = 0;
+          lap ^= 1u;
+        }
       }
-      umma_commit(done);
-      mbar_wait(done, 0, drain, SITE_DONE);
+      if (elect_one()) umma_commit(done);
+      warp_wait(done, 0, drain, SITE_DONE);
     }
   } else {
-    // elementwise: thread = key = TMEM lane; warpgroup w takes query rows 32 w .. 32 w + 31 of every tile
-    const int w = warp >> 2, row = (warp & 3) * 32 + lane, key = key0 + row;
+    // elementwise: thread = key = TMEM lane; warpgroup w takes PER query rows of its tiles
+    const int w = warp >> 2, p = NB == 2 ? w >> 1 : 0, part = NB == 2 ? w & 1 : w;
+    const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const uint32_t t = tmem + lane_off + 32 * w;
+    const uint32_t t = tmem + lane_off + Lay::BUF * p + Lay::PER * part;
     const uint64_t sl2 = f2_pack(g.scale_log2, g.scale_log2);
+    const int key = key0 + row;   // of a causal sequence
     bool ok = true;
-    for (int j = 0; j < n; ++j) {
-      const int st = j % NS, r0 = (j0 + j) * kStream;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&st_full[st], (j / NS) & 1, wc, SITE_ST_FULL));   // the row constants
-      ok = ok && __all_sync(0xFFFFFFFFu, mbar_wait(s_full, j & 1, wc, SITE_S_FULL));
+    for (int j = p; j < n; j += NB) {
+      const int st = j % NS, round = NB == 2 ? j >> 1 : j;
+      ok = warp_wait(&st_full[st], (j / NS) & 1, wc, SITE_ST_FULL);   // the row constants
+      ok = ok && warp_wait(&s_full[p], round & 1, wc, SITE_S_FULL);
       if (!ok) break;
       tc_fence_after();
-      uint32_t s1[32], s2[32], dp[32];
-      tmem_ld32(t + Lay::S1, s1);
-      tmem_ld32(t + Lay::S2, s2);
-      tmem_ld32(t + Lay::DP, dp);
-      tmem_wait_ld();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(s_free);   // the next tile's products may overwrite them
-      const float* cs = reinterpret_cast<const float*>(smem + Lay::OFF_ST + st * Lay::STAGE + 2 * TQ::BYTES + TO::BYTES) + 32 * w;
-      // rows behind the last one, or (causal) before the first that sees the whole tile
-      if (r0 < full || r0 + kStream > rows) {
-        const int* seen = reinterpret_cast<const int*>(cs + kRowSeen * kStream);
+      const float* cs =
+          reinterpret_cast<const float*>(smem + Lay::OFF_ST + st * Lay::STAGE + 2 * TQ::BYTES + TO::BYTES) + Lay::PER * part;
+      const int x0 = (j0 + j) * g.tcq;                 // first query of the box
+      const bool edge = g.causal && x0 < full;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (key >= seen[i]) s1[i] = s2[i] = 0xFF800000u;   // -inf: P = 0
-      }
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {   // eight query rows: 16 bytes of each operand row
-        uint32_t pp[4], x1[4], x2[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int i = 8 * q + 2 * e;
-          const uint64_t* pair = reinterpret_cast<const uint64_t*>(cs + i);
-          const uint64_t L1 = pair[kRowL1 * kStream / 2], L2 = pair[kRowL2 * kStream / 2], D1 = pair[kRowD1 * kStream / 2],
-                         D2 = pair[kRowD2 * kStream / 2], NL = pair[kRowLam * kStream / 2];
-          const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])), sl2, L1);
-          const uint64_t y2 = f2_fma(f2_pack(__uint_as_float(s2[i]), __uint_as_float(s2[i + 1])), sl2, L2);
-          const uint64_t dd = f2_pack(__uint_as_float(dp[i]), __uint_as_float(dp[i + 1]));
-          float a0, a1, b0, b1;
-          f2_unpack(y1, a0, a1);
-          f2_unpack(y2, b0, b1);
-          const uint64_t p1 = f2_pack(ex2_approx(a0), ex2_approx(a1));
-          const uint64_t p2 = f2_mul(f2_pack(ex2_approx(b0), ex2_approx(b1)), NL);
-          f2_unpack(f2_add(p1, p2), a0, a1);
-          pp[e] = diff_pack<F16>(a0, a1);
-          f2_unpack(f2_mul(p1, f2_add(dd, D1)), a0, a1);
-          x1[e] = diff_pack<F16>(a0, a1);
-          f2_unpack(f2_mul(p2, f2_add(dd, D2)), b0, b1);
-          x2[e] = diff_pack<F16>(b0, b1);
+      for (int cc = 0; cc < NB; ++cc) {
+        uint32_t s1[16], s2[16], dp[16];
+        tmem_ld16(t + 16 * cc, s1);
+        tmem_ld16(t + Lay::S2 + 16 * cc, s2);
+        tmem_ld16(t + Lay::DP + 16 * cc, dp);
+        tmem_wait_ld();
+        if (cc == NB - 1) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[p]);   // the next products may overwrite them
         }
-        if (q == 0 && j >= 1) {
-          // the products of the tile before have read P^T and dS^T
-          ok = __all_sync(0xFFFFFFFFu, mbar_wait(x_free, (j - 1) & 1, wc, SITE_X_DONE));
-          if (!ok) break;
+        if (edge) {
+          // query x sees the keys up to x + wk - wq
+          const int from = key - s.wk + s.wq - x0;   // the first query of the box that sees this key
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int r6 = Lay::PER * part + 16 * cc + i, x = g.group_magic ? div_by(r6, g.group_magic) : r6;
+            if (x < from) s1[i] = s2[i] = 0xFF800000u;   // -inf: P = 0
+          }
         }
-        uint8_t* to = smem + Lay::OFF_X + TP::offset(row, 4 * w + q);
-        *reinterpret_cast<uint4*>(to) = make_uint4(pp[0], pp[1], pp[2], pp[3]);
-        *reinterpret_cast<uint4*>(to + TP::BYTES) = make_uint4(x1[0], x1[1], x1[2], x1[3]);
-        *reinterpret_cast<uint4*>(to + 2 * TP::BYTES) = make_uint4(x2[0], x2[1], x2[2], x2[3]);
+        uint8_t* to = smem + Lay::OFF_X + p * Lay::X;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {   // eight query rows: 16 bytes of each operand row
+          uint32_t pp[4], x1[4], x2[4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {   // four rows' constants a load
+            const int i = 8 * q + 4 * e;
+            const ulonglong2* quad = reinterpret_cast<const ulonglong2*>(cs + 16 * cc + i);
+            const ulonglong2 L1 = quad[kRowL1 * 16], L2 = quad[kRowL2 * 16], D1 = quad[kRowD1 * 16], D2 = quad[kRowD2 * 16],
+                             NL = quad[kRowLam * 16];
+#pragma unroll
+            for (int f = 0; f < 2; ++f) {
+              const int at = i + 2 * f;
+              const uint64_t dd = raw_pair(dp + at);
+              const uint64_t y1 = f2_fma(raw_pair(s1 + at), sl2, f ? L1.y : L1.x), y2 = f2_fma(raw_pair(s2 + at), sl2, f ? L2.y : L2.x);
+              const bool poly = 2 * e + f + 4 * q < POLY;
+              const uint64_t p1 = poly ? exp2_pair<true>(y1) : exp2_pair<false>(y1);
+              const uint64_t p2 = f2_mul(poly ? exp2_pair<true>(y2) : exp2_pair<false>(y2), f ? NL.y : NL.x);
+              pp[2 * e + f] = pack_pair<F16>(f2_add(p1, p2));
+              x1[2 * e + f] = pack_pair<F16>(f2_mul(p1, f2_add(dd, f ? D1.y : D1.x)));
+              x2[2 * e + f] = pack_pair<F16>(f2_mul(p2, f2_add(dd, f ? D2.y : D2.x)));
+            }
+          }
+          if (cc == 0 && q == 0 && round >= 1) {
+            // the products of the buffer's tile before have read P^T and dS^T
+            ok = warp_wait(&x_free[p], (round - 1) & 1, wc, SITE_X_DONE);
+            if (!ok) break;
+          }
+          uint8_t* at = to + TP::offset(row, (Lay::PER * part + 16 * cc) / 8 + q);
+          *reinterpret_cast<uint4*>(at) = make_uint4(pp[0], pp[1], pp[2], pp[3]);
+          *reinterpret_cast<uint4*>(at + TP::BYTES) = make_uint4(x1[0], x1[1], x1[2], x1[3]);
+          *reinterpret_cast<uint4*>(at + 2 * TP::BYTES) = make_uint4(x2[0], x2[1], x2[2], x2[3]);
+        }
+        if (!ok) break;
       }
       if (!ok) break;
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(x_full);
+      if (lane == 0) mbar_arrive(&x_full[p]);
     }
-    if (ok && n > 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(done, 0, wc, SITE_DONE));
+    if (ok && n > 0) ok = warp_wait(done, 0, wc, SITE_DONE);
     tc_fence_after();
     if (ok && *abort_flag == 0u) {
-      const bool live = key < all, real = n > 0 && key < s.nk;   // keys behind the length have gradient zero
-      const long long token = live ? s.token(key) : 0;
-      auto store = [&](uint32_t col, int c0, int c1, uint16_t* out, int width, float f) {
-        for (int c = c0; c < c1; c += 16) {
-          uint32_t v[16];
-          tmem_ld16(tmem + lane_off + col + c, v);
+      // this lane's key
+      const int box = 2 * kt + (row >> 6), c = row & 63, by = box / k_nx;
+      const int x = (box - by * k_nx) * g.tck + (c & (g.tck - 1)), y = by * g.trk + (c >> g.lk);
+      const bool live = x < all && y < s.hk, real = n > 0 && x < s.wk;   // keys behind the length have gradient zero
+      const int token = live ? s.token(x, y) : 0;
+      // warpgroup w stores its quarter of the columns of each gradient
+      auto store = [&](uint32_t col, int cols, uint16_t* out, int width, float f) {
+        const int share = cols >= 32 ? cols / 4 : 8;
+        for (int c0 = w * share; c0 < min(cols, (w + 1) * share); c0 += 8) {
+          uint32_t v[8], o[4];
+          tmem_ld8(tmem + lane_off + col + c0, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t o[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int i = 8 * h + 2 * e;
-              o[e] = real ? diff_pack<F16>(__uint_as_float(v[i]) * f, __uint_as_float(v[i + 1]) * f) : 0u;
-            }
-            if (live && c + 8 * h < width) *reinterpret_cast<uint4*>(out + c + 8 * h) = make_uint4(o[0], o[1], o[2], o[3]);
-          }
+          for (int e = 0; e < 4; ++e)
+            o[e] = real ? diff_pack<F16>(__uint_as_float(v[2 * e]) * f, __uint_as_float(v[2 * e + 1]) * f) : 0u;
+          if (live && c0 < width) *reinterpret_cast<uint4*>(out + c0) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       };
-      store(Lay::V, w * (DV / 2), (w + 1) * (DV / 2), static_cast<uint16_t*>(a.dv) + s.b * g.v.b + token * g.v.t + hk * g.v.h, g.dv,
-            kUnshift<F16>);
-      store(w ? Lay::K2 : Lay::K1, 0, D, static_cast<uint16_t*>(w ? a.dk2 : a.dk1) + s.b * g.k.b + token * g.k.t + hk * g.k.h, g.d,
-            g.scale * kUnshift<F16>);
+      const long long kv = s.b * g.v.b + wide(token, g.v.t) + wide(hk, g.v.h), kk = s.b * g.k.b + wide(token, g.k.t) + wide(hk, g.k.h);
+      store(Lay::V, DV, static_cast<uint16_t*>(a.dv) + kv, g.dv, kUnshift<F16>);
+      store(Lay::K1, D, static_cast<uint16_t*>(a.dk1) + kk, g.d, g.scale * kUnshift<F16>);
+      store(Lay::K2, D, static_cast<uint16_t*>(a.dk2) + kk, g.d, g.scale * kUnshift<F16>);
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8) {
+  if (warp == kWarpS) {
     tc_fence_after();
     tmem_dealloc(tmem, Lay::COLS);
   }
@@ -660,30 +773,36 @@ __global__ void __launch_bounds__(kThreads, 1) diff_attn_dkv_kernel(const DiffBw
 template <int D, int DV, bool F16>
 cudaError_t launch_class(const DiffBwdArgs& a, cudaStream_t stream) {
   const DiffGeom& g = a.g;
-  const long long seqs = diff_sequences(g), units = seqs * g.kv_heads;
-  const int q_tiles = static_cast<int>((diff_max_rows(g) + kOwn - 1) / kOwn), k_tiles = (diff_max_keys(g) + kOwn - 1) / kOwn;
+  const long long units = static_cast<long long>(diff_sequences(g)) * g.kv_heads;
+  const int q_tiles = a.boxes / 2, k_tiles = ceil_div(diff_max_k_boxes(g), 2);
   constexpr int LPR = DV / 8;
-  const long long row_ctas = units * (a.rows_pad / (256 / LPR)), q_ctas = units * q_tiles, k_ctas = units * k_tiles + g.q_heads;
+  const long long row_ctas = units * a.boxes * LPR / 4, q_ctas = units * q_tiles, k_ctas = units * k_tiles + g.q_heads;
   if (row_ctas > 0x7FFFFFFFll || q_ctas > 0x7FFFFFFFll || k_ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  auto dq = diff_attn_dq_kernel<D, DV, F16>;
-  auto dkv = diff_attn_dkv_kernel<D, DV, F16>;
+  using TK = DiffTile<kOwn, D>;
+  using TV = DiffTile<kOwn, DV>;
+  CUtensorMap q1, q2, dO, k1, k2, v;
+  if (!diff_map(&q1, g, true, F16, a.q1, g.q, g.d, TK::COLS) || !diff_map(&q2, g, true, F16, a.q2, g.q, g.d, TK::COLS) ||
+      !diff_map(&dO, g, true, F16, a.dO, g.o, g.dv, TV::COLS) || !diff_map(&k1, g, false, F16, a.k1, g.k, g.d, TK::COLS) ||
+      !diff_map(&k2, g, false, F16, a.k2, g.k, g.d, TK::COLS) || !diff_map(&v, g, false, F16, a.v, g.v, g.dv, TV::COLS))
+    return cudaErrorInvalidValue;
+  auto dq = diff_attn_dq_kernel<D, DV, F16, RIB_DIFF_POLY_Q>;
+  auto dkv = diff_attn_dkv_kernel<D, DV, F16, RIB_DIFF_POLY_K>;
   cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLay<D, DV>::ALLOC);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvLay<D, DV>::ALLOC);
   if (e != cudaSuccess) return e;
   if (row_ctas > 0) {
     diff_attn_rows_kernel<LPR, F16><<<static_cast<unsigned>(row_ctas), 256, 0, stream>>>(a);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    dq<<<static_cast<unsigned>(q_ctas), kThreads, DqLay<D, DV>::ALLOC, stream>>>(a, q_tiles);
+    dq<<<static_cast<unsigned>(q_ctas), kThreads, DqLay<D, DV>::ALLOC, stream>>>(q1, q2, dO, k1, k2, v, a, q_tiles);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
   }
   // k_tiles 0: dlambda alone, with no tiles before it
-  dkv<<<static_cast<unsigned>(k_ctas), kThreads, DkvLay<D, DV>::ALLOC, stream>>>(a, k_tiles > 0 ? k_tiles : 1, k_tiles > 0 ? static_cast<int>(units) : 0);
+  dkv<<<static_cast<unsigned>(k_ctas), kThreads, DkvLay<D, DV>::ALLOC, stream>>>(q1, q2, dO, k1, k2, v, a, k_tiles > 0 ? k_tiles : 1,
+                                                                               k_tiles > 0 ? static_cast<int>(units) : 0);
   return cudaGetLastError();
 }
 
 }  // namespace
-
-long long diff_rows_pad(const DiffGeom& g) { return (diff_max_rows(g) + kOwn - 1) / kOwn * kOwn; }
 
 cudaError_t launch_diff_attn_bwd(const DiffBwdArgs& a, bool f16, cudaStream_t stream) {
   switch (diff_class(a.g.d, a.g.dv)) {

@@ -19,8 +19,8 @@
 //                        NG = 2, one group a map.
 //   then one warp        TMEM owner, issues S
 //   then one warp        issues P V (its own stream: neither waits for the other)
-//   then kLoadWarps      loaders: cp.async rows into swizzled tiles (any strides,
-//                        windows cut anywhere; masked keys become zero rows)
+//   then one warp        TMA producer
+//   then one warp        clears the rows of a key box that are not the sequence's
 // TMEM: S of map m and parity q at 64 (2 q + m), O from column 256.
 //
 // Bound: the exponentials, 2 per (query, key) pair: a tile of 128 x 64 x 2
@@ -39,7 +39,7 @@ namespace {
 constexpr int kBK = 64;
 
 enum Site : int {
-  SITE_Q = 401, SITE_KV_FULL = 402, SITE_KV_EMPTY = 403, SITE_S = 404, SITE_P = 405, SITE_PV = 406, SITE_DONE = 407,
+  SITE_RAW = 400, SITE_Q = 401, SITE_KV_FULL = 402, SITE_KV_EMPTY = 403, SITE_S = 404, SITE_P = 405, SITE_PV = 406, SITE_DONE = 407,
 };
 
 template <int D, int DV>
@@ -49,14 +49,13 @@ struct FwdLay {
   using TV = DiffTile<kBK, DV>;
   static constexpr int NP = DV <= 64 ? 2 : 1;               // O accumulators of a map
   static constexpr int NG = 2 * NP;
-  static constexpr int kLoadWarps = 2;
-  static constexpr int kThreads = 32 * (4 * NG + 2 + kLoadWarps);
+  static constexpr int kThreads = 32 * (4 * NG + 4);
   static constexpr int STAGE = 2 * TK::BYTES + TV::BYTES;
   static constexpr int NS = STAGE <= 16 * 1024 ? 6 : 4;
   static constexpr int OFF_ST = 2 * TQ::BYTES;
   static constexpr int OFF_L = OFF_ST + NS * STAGE;         // [4][128] m, then [4][128] l of each group
   static constexpr int OFF_BAR = OFF_L + 2 * 4 * 128 * 4;
-  static constexpr int NBAR = 1 + 2 * NS + 12 + 1;          // q, kv_full, kv_empty, s[4], p[4], pv[4], done
+  static constexpr int NBAR = 1 + 3 * NS + 12 + 1;          // q, kv_full, kv_empty, raw, s[4], p[4], pv[4], done
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
   static constexpr uint32_t O = 256, COLS = 512;
@@ -74,19 +73,23 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 template <int D, int DV, bool F16, int POLY>
-__global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kernel(const DiffFwdArgs a, int q_tiles) {
+__global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1)
+diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
+                     const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
+                     const __grid_constant__ CUtensorMap tm_v, const DiffFwdArgs a, int q_tiles) {
   using Lay = FwdLay<D, DV>;
   using TQ = typename Lay::TQ;
   using TK = typename Lay::TK;
   using TV = typename Lay::TV;
-  constexpr int NS = Lay::NS, NP = Lay::NP, NG = Lay::NG, kLoadWarps = Lay::kLoadWarps, kLoaders = 32 * kLoadWarps;
-  constexpr int kWarpS = 4 * NG, kWarpPV = kWarpS + 1, kWarpLoad = kWarpS + 2;
+  constexpr int NS = Lay::NS, NP = Lay::NP, NG = Lay::NG;
+  constexpr int kWarpS = 4 * NG, kWarpPV = kWarpS + 1, kWarpLoad = kWarpS + 2, kWarpClear = kWarpS + 3;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = align_smem_1024(smem_raw);
   uint64_t* q_full = reinterpret_cast<uint64_t*>(smem + Lay::OFF_BAR);
   uint64_t* kv_full = q_full + 1;
   uint64_t* kv_empty = kv_full + NS;
-  uint64_t* s_full = kv_empty + NS;   // [2 q + m], as the two below
+  uint64_t* raw = kv_empty + NS;      // loaded, to be cleared (used instead of kv_full then)
+  uint64_t* s_full = raw + NS;        // [2 q + m], as the two below
   uint64_t* p_full = s_full + 4;
   uint64_t* pv = s_full + 8;
   uint64_t* done = s_full + 12;
@@ -103,17 +106,21 @@ __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kern
   u /= q_tiles;
   const int hk = u % g.kv_heads;
   const DiffSeq s = diff_sequence(g, u / g.kv_heads);
-  const int rows = s.nq * g.group, row0 = qt * 128;
-  if (row0 >= rows) return;   // a window at the map's edge has fewer tiles
-  const int last_t = diff_row_token(g, min(row0 + 128, rows) - 1);
-  const int tiles = (diff_visible(g, s, last_t) + kBK - 1) / kBK;
+  const int q_boxes = diff_q_boxes(g, s);
+  if (2 * qt >= q_boxes) return;   // a window at the map's edge has fewer tiles
+  // key boxes: all, or (causal) those that the last row sees
+  const int k_nx = g.causal ? ceil_div(diff_visible(g, s, min((2 * qt + 2) * g.tcq, s.wq) - 1), g.tck) : ceil_div(s.wk, g.tck);
+  const int tiles = k_nx * ceil_div(s.hk, g.trk);
+  const bool cut = s.wk % g.tck || s.hk % g.trk;            // some boxes are not the sequence's alone
+  const bool clear = cut && (g.window || g.k_lens);         // what lies behind a tensor's end arrives as zeros
   const int per = (tiles + a.splits - 1) / a.splits;
   const int j0 = sp * per, n = max(0, min(tiles, j0 + per) - j0);
 
   if (threadIdx.x == 0) {
-    mbar_init(q_full, kLoadWarps);
+    mbar_init(q_full, 1);
     for (int i = 0; i < NS; ++i) {
-      mbar_init(&kv_full[i], kLoadWarps);
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&raw[i], 1);
       mbar_init(&kv_empty[i], 1);
     }
     for (int i = 0; i < 4; ++i) {
@@ -130,121 +137,149 @@ __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kern
     tmem_alloc(tmem_holder, Lay::COLS);
     tmem_relinquish();
   }
+  const int q_rows = g.tcq * g.trq * g.group;   // of a box
+  if (q_rows < 64) {
+    // rows that no load writes: zeros, so that their scores stay finite
+    for (int i = threadIdx.x * 16; i < Lay::OFF_ST; i += Lay::kThreads * 16) *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
+    fence_proxy_async_smem();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
   const WaitCtx wc{abort_flag, a.err};
+  const WaitCtx drain{tmem_holder + 2, a.err};
 
-  if (warp >= kWarpLoad) {
-    // ------------------------------------------------------------ loaders
-    const int tid = threadIdx.x - kWarpLoad * 32;
-    const uint32_t sq = smem_u32(smem), sst = sq + Lay::OFF_ST;
-    const uint16_t* q1 = static_cast<const uint16_t*>(a.q1) + s.b * g.q.b + static_cast<long long>(hk) * g.group * g.q.h;
-    const uint16_t* q2 = static_cast<const uint16_t*>(a.q2) + s.b * g.q.b + static_cast<long long>(hk) * g.group * g.q.h;
-    const uint16_t* k1 = static_cast<const uint16_t*>(a.k1) + s.b * g.k.b + hk * g.k.h;
-    const uint16_t* k2 = static_cast<const uint16_t*>(a.k2) + s.b * g.k.b + hk * g.k.h;
-    const uint16_t* v = static_cast<const uint16_t*>(a.v) + s.b * g.v.b + hk * g.v.h;
-    int told = -1;   // the last load whose barrier this warp has arrived on (-1: none, 0: Q, i + 1: key tile i)
-    auto tell = [&](int upto) {
-      if (upto <= told) return;
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0)
-        for (int i = told + 1; i <= upto; ++i) mbar_arrive(i == 0 ? q_full : &kv_full[(i - 1) % NS]);
-      told = upto;
-    };
-    if (n > 0) {
-      diff_clear<D, DV, kLoaders>(smem, Lay::OFF_L, g, tid);
-      diff_load_queries<128, D, DV, kLoaders>(sq, q1, q2, nullptr, g, s, row0, rows, tid);
-      cp_async_commit();
-    }
-    for (int i = 0; i < n; ++i) {
-      const int st = i % NS;
-      if (i >= NS) {
-        const uint32_t parity = ((i / NS) - 1) & 1;
-        if (!__all_sync(0xFFFFFFFFu, mbar_test_wait(&kv_empty[st], parity))) {
-          // about to wait: first hand over everything that is on its way
-          cp_async_wait<0>();
-          tell(i);
-          if (!__all_sync(0xFFFFFFFFu, mbar_wait(&kv_empty[st], parity, wc, SITE_KV_EMPTY))) break;
+  if (warp == kWarpLoad) {
+    // --------------------------------------------------------- TMA producer
+    if (lane == 0 && n > 0) {
+      const int nx_q = ceil_div(s.wq, g.tcq), halves = min(2, q_boxes - 2 * qt);
+      mbar_arrive_expect_tx(q_full, 2 * halves * TQ::box_bytes(q_rows));
+      for (int h = 0; h < halves; ++h) {
+        const int box = 2 * qt + h, by = box / nx_q, x = s.x0 + (box - by * nx_q) * g.tcq, y = s.y0 + by * g.trq;
+        TQ::load(smem, h, &tm_q1, q_full, hk * g.group, x, y, s.b);
+        TQ::load(smem + TQ::BYTES, h, &tm_q2, q_full, hk * g.group, x, y, s.b);
+      }
+      const uint32_t bytes = 2 * TK::box_bytes(kBK) + TV::box_bytes(kBK);
+      int by = j0 / k_nx, bx = j0 - by * k_nx, issued = 0;
+      uint64_t* full = clear ? raw : kv_full;
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (i >= NS && !mbar_wait(&kv_empty[st], ((i / NS) - 1) & 1, wc, SITE_KV_EMPTY)) break;
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        const int x = s.x0 + bx * g.tck, y = s.y0 + by * g.trk;
+        mbar_arrive_expect_tx(&full[st], bytes);
+        TK::load(to, 0, &tm_k1, &full[st], hk, x, y, s.b);
+        TK::load(to + TK::BYTES, 0, &tm_k2, &full[st], hk, x, y, s.b);
+        TV::load(to + 2 * TK::BYTES, 0, &tm_v, &full[st], hk, x, y, s.b);
+        issued = i + 1;
+        if (++bx == k_nx) {
+          bx = 0;
+          ++by;
         }
       }
-      const uint32_t b = sst + st * Lay::STAGE;
-      const int first = (j0 + i) * kBK;
-      diff_load_keys<kBK, D, DV, kLoaders>(b, k1, k2, v, g, s, first, s.nk, tid);
-      cp_async_commit();
-      cp_async_wait<2>();
-      tell(i - 1);   // all but the two newest groups
+      // nothing is left in flight when the CTA ends
+      mbar_wait(q_full, 0, drain, SITE_DONE);
+      for (int i = max(0, issued - NS); i < issued; ++i) mbar_wait(&full[i % NS], (i / NS) & 1, drain, SITE_DONE);
     }
-    cp_async_wait<0>();
-    if (n > 0 && *abort_flag == 0u) tell(n);
+  } else if (warp == kWarpClear) {
+    // ------------------------------------------------------------- clearing
+    if (clear)
+      for (int i = 0; i < n; ++i) {
+        const int st = i % NS;
+        if (!warp_wait(&raw[st], (i / NS) & 1, wc, SITE_RAW)) break;
+        const DiffKeyBox k = diff_key_box(g, s, k_nx, j0 + i);
+        const uint64_t mask = diff_key_mask(g, k.vx, k.vy);
+        uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
+        if (mask != ~0ull) {
+          for (int row = 0; row < kBK; ++row)
+            if (!((mask >> row) & 1ull)) {
+              TK::clear_row(to, row, lane, 32);
+              TK::clear_row(to + TK::BYTES, row, lane, 32);
+              TV::clear_row(to + 2 * TK::BYTES, row, lane, 32);
+            }
+          fence_proxy_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&kv_full[st]);
+      }
   } else if (warp == kWarpS) {
     // --------------------------------------------------------- S issuer
-    if (lane == 0 && n > 0) {
-      const uint32_t sq = smem_u32(smem), sst = sq + Lay::OFF_ST;
+    if (n > 0) {
+      const uint32_t sq = smem_u32(smem);
       const uint32_t id_s = diff_idesc(F16, kBK, false);
-      const int ks_d = (g.d + 15) / 16;
-      bool ok = mbar_wait(q_full, 0, wc, SITE_Q);
+      const uint64_t dq[2] = {TQ::kmajor(sq), TQ::kmajor(sq + TQ::BYTES)}, dk = TK::kmajor(sq + Lay::OFF_ST);
+      bool ok = warp_wait(q_full, 0, wc, SITE_Q);
+      int st = 0;
+      uint32_t lap = 0;   // parity of the stages' lap
       for (int j = 0; ok && j < n; ++j) {
-        if (!(ok = mbar_wait(&kv_full[j % NS], (j / NS) & 1, wc, SITE_KV_FULL))) break;
+        ok = warp_wait(&kv_full[st], lap, wc, SITE_KV_FULL);
+        const uint64_t k = dk + static_cast<uint32_t>(st) * (Lay::STAGE >> 4);
+#pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int b = 2 * (j & 1) + m;
           // S overwrites the P of two tiles before: its product has to be done with it
-          if (j >= 2 && !(ok = mbar_wait(&pv[b], ((j - 2) >> 1) & 1, wc, SITE_PV))) break;
-          tc_fence_after();
-          const uint32_t q = sq + m * TQ::BYTES, k = sst + (j % NS) * Lay::STAGE + m * TK::BYTES;
-#pragma unroll
-          for (int ks = 0; ks < D / 16; ++ks)
-            if (ks < ks_d) umma_ss(tmem + 64u * b, TQ::kmajor(q, ks), TK::kmajor(k, ks), id_s, ks > 0 ? 1u : 0u);
-          umma_commit(&s_full[b]);
+          if (ok && j >= 2) ok = warp_wait(&pv[b], ((j - 2) >> 1) & 1, wc, SITE_PV);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            diff_mma_kk<TQ, TK, D / 16>(tmem + 64u * b, dq[m], k + m * (TK::BYTES >> 4), id_s);
+            umma_commit(&s_full[b]);
+          }
+          __syncwarp();
+        }
+        if (++st == NS) {
+          st = 0;
+          lap ^= 1u;
         }
       }
-      umma_commit(done);
-      const WaitCtx drain{tmem_holder + 2, a.err};
-      mbar_wait(done, 0, drain, SITE_DONE);
+      if (elect_one()) umma_commit(done);
+      warp_wait(done, 0, drain, SITE_DONE);
     }
   } else if (warp == kWarpPV) {
     // ------------------------------------------------------- P V issuer
-    if (lane == 0 && n > 0) {
-      const uint32_t sst = smem_u32(smem) + Lay::OFF_ST;
+    if (n > 0) {
       const uint32_t id_o = diff_idesc(F16, (g.dv + 15) / 16 * 16, true);
+      const uint64_t dv = TV::mnmajor(smem_u32(smem) + Lay::OFF_ST + 2 * TK::BYTES);
       bool ok = true;
+      int st = 0;
       for (int j = 0; ok && j < n; ++j) {
-        const uint32_t vb = sst + (j % NS) * Lay::STAGE + 2 * TK::BYTES;
+        const uint64_t v = dv + static_cast<uint32_t>(st) * (Lay::STAGE >> 4);
+#pragma unroll
         for (int m = 0; m < 2; ++m) {
           const int b = 2 * (j & 1) + m;
-          if (!(ok = mbar_wait(&p_full[b], (j >> 1) & 1, wc, SITE_P))) break;
-          tc_fence_after();
-          const uint32_t o = tmem + Lay::O + DV * (NP == 2 ? b : m);
+          ok = ok && warp_wait(&p_full[b], (j >> 1) & 1, wc, SITE_P);
+          if (ok && elect_one()) {
+            tc_fence_after();
+            const uint32_t o = tmem + Lay::O + DV * (NP == 2 ? b : m), p = tmem + 64u * b, acc = j >= NP ? 1u : 0u;
 #pragma unroll
-          for (int ks = 0; ks < kBK / 16; ++ks)
-            umma_ts(o, tmem + 64u * b + 8u * ks, TV::mnmajor(vb, ks), id_o, (j >= NP || ks > 0) ? 1u : 0u);
-          umma_commit(&pv[b]);
-          if (m == 1) umma_commit(&kv_empty[j % NS]);   // S of the tile was done before its P was written
+            for (int ks = 0; ks < kBK / 16; ++ks) umma_ts(o, p + 8u * ks, v + TV::mnstep(ks), id_o, ks > 0 ? 1u : acc);
+            umma_commit(&pv[b]);
+            if (m == 1) umma_commit(&kv_empty[st]);   // S of the tile was done before its P was written
+          }
+          __syncwarp();
         }
+        if (++st == NS) st = 0;
       }
-      umma_commit(done);
-      const WaitCtx drain{tmem_holder + 2, a.err};
-      mbar_wait(done, 0, drain, SITE_DONE);
+      if (elect_one()) umma_commit(done);
+      warp_wait(done, 0, drain, SITE_DONE);
     }
   } else {
     // ------------------------------------------------------------ softmax
     const int gi = warp >> 2, m = gi & 1, p = gi >> 1;   // map and, with NP = 2, the parity of its tiles
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const int r = row0 + row;
-    const bool live = r < rows;
-    const int t = diff_row_token(g, r), hq = hk * g.group + (r - t * g.group);
-    const int seen = live ? diff_visible(g, s, t) : 0;
-    const bool warp_live = row0 + (warp & 3) * 32 < rows;   // a warp without rows only keeps the barriers going
+    const DiffRow q = diff_query_row(g, s, 2 * qt + (row >> 6), row & 63);
+    const bool live = q.live;
+    const int hq = hk * g.group + q.head;
+    const int seen = live ? diff_visible(g, s, q.x) : 0x7FFFFFFF;   // of a sequence
+    const bool warp_live = __any_sync(0xFFFFFFFFu, live);            // a warp without rows only keeps the barriers going
     const float sl2 = g.scale_log2;
     float mx = -INFINITY, l = 0.f;
     bool ok = true;
     for (int j = p; j < n; j += NP) {
       const int b = 2 * (j & 1) + m;
       const uint32_t tS = tmem + lane_off + 64u * b;
-      ok = __all_sync(0xFFFFFFFFu, mbar_wait(&s_full[b], (j >> 1) & 1, wc, SITE_S));
+      ok = warp_wait(&s_full[b], (j >> 1) & 1, wc, SITE_S);
       if (!ok) break;
       tc_fence_after();
       if (warp_live) {
@@ -252,13 +287,16 @@ __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kern
         tmem_ld32(tS, sv[0]);
         tmem_ld32(tS + 32, sv[1]);
         tmem_wait_ld();
-        const int left = seen - (j0 + j) * kBK;   // keys of this tile that the row sees
-        if (__any_sync(0xFFFFFFFFu, left < kBK)) {
+        if (cut || g.causal) {
+          const uint64_t mask = diff_seen(g, s, k_nx, j0 + j, seen);
+          if (__any_sync(0xFFFFFFFFu, mask != ~0ull)) {
+            const uint32_t bits[2] = {static_cast<uint32_t>(mask), static_cast<uint32_t>(mask >> 32)};
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (32 * c + i >= left) sv[c][i] = 0xFF800000u;
+              for (int i = 0; i < 32; ++i)
+                if (!(bits[c] & (1u << i))) sv[c][i] = 0xFF800000u;
+          }
         }
         float tops[4];
 #pragma unroll
@@ -323,7 +361,7 @@ __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kern
       if (lane == 0) mbar_arrive(&p_full[b]);
     }
     const int last = n - 1 - (NP == 2 ? (n - 1 - p) & 1 : 0);   // this group's last tile (negative: none)
-    if (ok && last >= 0) ok = __all_sync(0xFFFFFFFFu, mbar_wait(&pv[2 * (last & 1) + m], (last >> 1) & 1, wc, SITE_PV));
+    if (ok && last >= 0) ok = warp_wait(&pv[2 * (last & 1) + m], (last >> 1) & 1, wc, SITE_PV);
     tc_fence_after();
     float* sm = reinterpret_cast<float*>(smem + Lay::OFF_L);
     sm[gi * 128 + row] = mx;
@@ -349,16 +387,16 @@ __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1) diff_attn_fwd_kern
         for (int k = 0; k < NP; ++k) cf[2 * k + i] *= inv;
         lse2[i] = sum == 0.f ? -INFINITY : ref + log2f(sum);
       }
-      const long long prow = a.part ? ((static_cast<long long>(s.b) * g.kv_heads + hk) * g.q_len * g.group + r) : 0;   // window 0 only
+      const long long prow = a.part ? ((wide(s.b, g.kv_heads) + hk) * g.q_len + q.x) * g.group + q.head : 0;   // sequences only
       const long long prows = static_cast<long long>(g.batch) * g.q_heads * g.q_len;
-      const long long token = live ? s.token(t) : 0;
+      const int token = live ? s.token(q.x, q.y) : 0;
       if (live && gi < 2 && a.part)
         a.part[static_cast<long long>(a.splits) * prows * 2 * g.dv + (static_cast<long long>(sp) * prows + prow) * 2 + gi] = lse2[gi];
       if (live && gi < 2 && a.lse && !a.part)
         a.lse[((static_cast<long long>(gi) * g.batch + s.b) * g.q_heads + hq) * g.q_len + token] = lse2[gi] * kDiffLn2;
       const float lam = live ? diff_lambda<F16>(a.lam, g.lam_f32, hq) : 0.f;
-      uint16_t* o = static_cast<uint16_t*>(a.o) + s.b * g.o.b + token * g.o.t + hq * g.o.h;
-      uint16_t* o2 = a.o2 ? static_cast<uint16_t*>(a.o2) + s.b * g.o.b + token * g.o.t + hq * g.o.h : nullptr;
+      uint16_t* o = static_cast<uint16_t*>(a.o) + s.b * g.o.b + wide(token, g.o.t) + wide(hq, g.o.h);
+      uint16_t* o2 = a.o2 ? static_cast<uint16_t*>(a.o2) + s.b * g.o.b + wide(token, g.o.t) + wide(hq, g.o.h) : nullptr;
       // group gi stores its share of the columns
 #pragma unroll
       for (int c = 0; c < DV / NG / 8; ++c) {
@@ -455,7 +493,7 @@ __global__ void __launch_bounds__(256) diff_attn_join_kernel(const DiffFwdArgs a
     w[e] = F16 ? pack_f16x2_sat(d0, d1) : pack_bf16x2(d0, d1);
     w2[e] = F16 ? pack_f16x2_sat(f[1][2 * e], f[1][2 * e + 1]) : pack_bf16x2(f[1][2 * e], f[1][2 * e + 1]);
   }
-  const long long to = b * g.o.b + t * g.o.t + hq * g.o.h + c;
+  const long long to = b * g.o.b + wide(t, g.o.t) + wide(hq, g.o.h) + c;
   *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + to) = make_uint4(w[0], w[1], w[2], w[3]);
   if (a.o2) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o2) + to) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
   if (a.lse && c == 0)
@@ -471,11 +509,18 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
   auto kernel = diff_attn_fwd_kernel<D, DV, F16, POLY>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC);
   if (e != cudaSuccess) return e;
-  const int q_tiles = static_cast<int>((diff_max_rows(a.g) + 127) / 128);
-  const long long ctas = static_cast<long long>(diff_sequences(a.g)) * a.g.kv_heads * q_tiles * a.splits;
+  const DiffGeom& g = a.g;
+  const int q_tiles = ceil_div(diff_max_q_boxes(g), 2);
+  const long long ctas = static_cast<long long>(diff_sequences(g)) * g.kv_heads * q_tiles * a.splits;
   if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-  if (ctas == 0) return cudaSuccess;
-  kernel<<<static_cast<unsigned>(ctas), Lay::kThreads, Lay::ALLOC, stream>>>(a, q_tiles);
+  CUtensorMap q1, q2, k1, k2, v;
+  using TQ = typename Lay::TQ;
+  using TV = typename Lay::TV;
+  if (!diff_map(&q1, g, true, F16, a.q1, g.q, g.d, TQ::COLS) || !diff_map(&q2, g, true, F16, a.q2, g.q, g.d, TQ::COLS) ||
+      !diff_map(&k1, g, false, F16, a.k1, g.k, g.d, TQ::COLS) || !diff_map(&k2, g, false, F16, a.k2, g.k, g.d, TQ::COLS) ||
+      !diff_map(&v, g, false, F16, a.v, g.v, g.dv, TV::COLS))
+    return cudaErrorInvalidValue;
+  kernel<<<static_cast<unsigned>(ctas), Lay::kThreads, Lay::ALLOC, stream>>>(q1, q2, k1, k2, v, a, q_tiles);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
   const long long threads = static_cast<long long>(a.g.batch) * a.g.q_heads * a.g.q_len * (a.g.dv / 8);
   diff_attn_join_kernel<F16><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a);
@@ -488,11 +533,28 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
 // many splits as fill them, each of at least four tiles of keys.
 int diff_splits(const DiffGeom& g) {
   if (g.window || g.q_len == 0 || g.batch == 0) return 1;
-  const long long units = static_cast<long long>(g.batch) * g.kv_heads * ((diff_max_rows(g) + 127) / 128);
+  const long long units = static_cast<long long>(g.batch) * g.kv_heads * ceil_div(diff_max_q_boxes(g), 2);
   const long long tiles = (g.k_len + kBK - 1) / kBK;
   const long long want = 2 * sm_count() / units, most = tiles / 4;
   const long long s = want < most ? want : most;
   return s > 1 ? static_cast<int>(s < 64 ? s : 64) : 1;
+}
+
+bool diff_map(CUtensorMap* map, const DiffGeom& g, bool query, bool f16, const void* p, const DiffStrides& s, int e, int cols) {
+  const int heads = query ? g.q_heads : g.kv_heads, len = query ? g.q_len : g.k_len;
+  const uint64_t x = static_cast<uint64_t>(g.window ? g.width : len), y = static_cast<uint64_t>(g.window ? g.height : 1);
+  *map = CUtensorMap{};
+  if (len == 0 || g.batch == 0) return true;   // nothing to load
+  const uint64_t dims[5] = {static_cast<uint64_t>(e), static_cast<uint64_t>(heads), x, y, static_cast<uint64_t>(g.batch)};
+  const uint64_t raw[4] = {static_cast<uint64_t>(s.h) * 2, static_cast<uint64_t>(s.t) * 2, static_cast<uint64_t>(s.t) * 2 * x,
+                           static_cast<uint64_t>(s.b) * 2};
+  uint64_t strides[4];
+  for (int i = 0; i < 4; ++i) strides[i] = dims[i + 1] > 1 ? raw[i] : 16;   // an axis of one place is never stepped along
+  const uint32_t box[5] = {static_cast<uint32_t>(cols), static_cast<uint32_t>(query ? g.group : 1), static_cast<uint32_t>(query ? g.tcq : g.tck),
+                           static_cast<uint32_t>(query ? g.trq : g.trk), 1};
+  const CUtensorMapSwizzle sw = cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
+  return encode_tiled(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p), dims, strides, box,
+                      sw) == CUDA_SUCCESS;
 }
 
 size_t diff_split_bytes(const DiffGeom& g) {

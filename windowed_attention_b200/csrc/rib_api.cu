@@ -74,6 +74,8 @@ const char* site_name(int s) {
     case 307: return "attention backward: accumulate MMAs";
     case 308: return "attention backward: final MMA drain";
     case 309: return "attention backward: TMA drain";
+    case 400: return "differential attention: box loaded";
+    case 420: return "differential attention backward: box loaded";
     case 401: return "differential attention: queries loaded";
     case 402: return "differential attention: stage loaded";
     case 403: return "differential attention: free stage";
