@@ -197,4 +197,4 @@ def test_diff_attention_binding_refusals():
     with pytest.raises(ValueError):
         rib.diff_attn_desc(1, 4, 4, 2, 2, 16, 32, 0.25, torch.int32)
     with pytest.raises(ValueError):
-        _lib._strided_arg("q1", t, 4, 2, 16, d.q_stride, d, 0)
+        _lib._strided_arg("q1", t, (1, 4, 2, 16), None, d.dtype, 0)

@@ -158,10 +158,18 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None:
+            import torch
+            # the stream's handle without a Stream object around it, where torch offers that
+            get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
+            _raw_stream = (lambda: get(dev())) if get else (lambda: torch.cuda.current_stream().cuda_stream)
+        return _raw_stream()
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -402,19 +410,20 @@ def _code(dtype) -> int:
 
 def _current_device(t) -> int:
     import torch
-    if not t.is_cuda:
+    at = t.get_device()
+    if at < 0:
         raise ValueError("librib entry points take device tensors")
-    d = torch.cuda.current_device()
-    if t.device.index != d:
-        raise ValueError(f"tensor on {t.device} while the current device is cuda:{d}: make its device current for the call")
-    return d
+    if at != torch.cuda.current_device():
+        raise ValueError(f"tensor on {t.device} while the current device is cuda:{torch.cuda.current_device()}: "
+                         "make its device current for the call")
+    return at
 
 
 def _arg(name, t, numel, code, device) -> Optional[int]:
     """Pointer of a contiguous device tensor of at least `numel` values of type `code`; None stays None."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
     if _code(t.dtype) != code:
         raise ValueError(f"{name} is {t.dtype}")
@@ -427,10 +436,10 @@ def _arg(name, t, numel, code, device) -> Optional[int]:
 
 def _step_arg(step, device) -> Optional[int]:
     """Pointer of the device word added to a dropout offset."""
-    import torch
     if step is None:
         return None
-    if step.dtype not in (torch.int64, torch.uint64) or step.numel() < 1 or not step.is_cuda or step.device.index != device:
+    import torch
+    if step.dtype not in (torch.int64, torch.uint64) or step.numel() < 1 or step.get_device() != device:
         raise ValueError("step is one int64 or uint64 on the current device")
     return step.data_ptr()
 
@@ -492,8 +501,6 @@ def rib_residual_norm_bwd(desc: ResidualNormDesc, x_out, y=None, gate=None, scal
     d = desc
     dev = _current_device(x_out if x_out is not None else dx_out)
     n, C, xc, c, g = d.T * d.C, d.C, d.x_dtype, d.dtype, _norm_groups(d) * d.C
-    if workspace is not None and (not workspace.is_cuda or workspace.device.index != dev or not workspace.is_contiguous()):
-        raise ValueError("workspace is a contiguous tensor of the current device")
     _check(_lib.rib_residual_norm_bwd(
         ctypes.byref(d), _arg("x_out", x_out, n, xc, dev), _arg("y", y, n, c, dev), _arg("gate", gate, n, c, dev),
         _arg("scale", scale, g, RIB_F32, dev), _arg("post_w", post_w, C, RIB_F32, dev), _arg("post_b", post_b, C, RIB_F32, dev),
@@ -501,8 +508,7 @@ def rib_residual_norm_bwd(desc: ResidualNormDesc, x_out, y=None, gate=None, scal
         _arg("dx", dx, n, xc, dev), _arg("dy", dy, n, c, dev), _arg("dgate", dgate, n, c, dev),
         _arg("dscale", dscale, g, RIB_F32, dev), _arg("dpost_w", dpost_w, C, RIB_F32, dev),
         _arg("dpost_b", dpost_b, C, RIB_F32, dev), _arg("dpre_w", dpre_w, C, RIB_F32, dev),
-        _arg("dpre_b", dpre_b, C, RIB_F32, dev), None if workspace is None else workspace.data_ptr(),
-        0 if workspace is None else workspace.numel() * workspace.element_size(), _step_arg(step, dev), _stream(stream)))
+        _arg("dpre_b", dpre_b, C, RIB_F32, dev), *_workspace_arg(workspace, dev), _step_arg(step, dev), _stream(stream)))
 
 
 def diff_attn_desc(batch, q_len, k_len, q_heads, kv_heads, d, dv, scale, dtype, lam_dtype=None, causal=False, window=0, width=0,
@@ -517,46 +523,55 @@ def diff_attn_desc(batch, q_len, k_len, q_heads, kv_heads, d, dv, scale, dtype, 
                         float(scale), int(bool(causal)), window, width, *s)
 
 
-def _strided_arg(name, t, tokens, heads, width, strides, desc, device) -> Optional[int]:
-    """Pointer of a device tensor [batch, tokens, heads, width] laid out as the descriptor says."""
+def _strided_arg(name, t, shape, strides, desc_code, device) -> Optional[int]:
+    """Pointer of a device tensor [batch, tokens, heads, width] of that shape, laid out as the descriptor says."""
     if t is None:
         return None
-    if not t.is_cuda or t.device.index != device:
+    if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
-    if _TORCH_CODE.get(t.dtype) != desc.dtype:
+    if _TORCH_CODE.get(t.dtype) != desc_code:
         raise ValueError(f"{name} is {t.dtype}")
-    shape = (desc.batch, tokens, heads, width)
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the descriptor says {shape}")
-    if any(strides):
+    if strides is not None:
         want = (*strides, 1)
-        if any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
+        if t.stride() != want and any(n > 1 and a != b for n, a, b in zip(shape, t.stride(), want)):
             raise ValueError(f"{name} has strides {t.stride()}, the descriptor says {want}")
     elif not t.is_contiguous():
         raise ValueError(f"{name}: not contiguous, and the descriptor names no strides")
     return t.data_ptr()
 
 
+def _strides_of(field):
+    s = tuple(field)
+    return s if any(s) else None
+
+
 def _workspace_arg(ws, device):
     if ws is None:
         return None, 0
-    if not ws.is_cuda or ws.device.index != device or not ws.is_contiguous():
+    if ws.get_device() != device or not ws.is_contiguous():
         raise ValueError("workspace is a contiguous tensor of the current device")
     n = ws.numel() * ws.element_size()
     return (ws.data_ptr() if n else None), n
 
 
-def _diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev):
+def _diff_args(d, dev):
+    """Checkers of the query, key, value and output tensors of a descriptor."""
+    b, nq, nk, hq, hk, e, ev, code = d.batch, d.q_len, d.k_len, d.q_heads, d.kv_heads, d.d, d.dv, d.dtype
+    q, k, v, o = (b, nq, hq, e), (b, nk, hk, e), (b, nk, hk, ev), (b, nq, hq, ev)
+    sq, sk, sv, so = _strides_of(d.q_stride), _strides_of(d.k_stride), _strides_of(d.v_stride), _strides_of(d.o_stride)
+    return (lambda n, t: _strided_arg(n, t, q, sq, code, dev), lambda n, t: _strided_arg(n, t, k, sk, code, dev),
+            lambda n, t: _strided_arg(n, t, v, sv, code, dev), lambda n, t: _strided_arg(n, t, o, so, code, dev))
+
+
+def _lens_arg(k_lens, batch, device) -> Optional[int]:
     import torch
-    if k_lens is not None and (k_lens.dtype != torch.int32 or k_lens.numel() < d.batch or not k_lens.is_cuda or
-                               k_lens.device.index != dev or not k_lens.is_contiguous()):
+    if k_lens is None:
+        return None
+    if k_lens.dtype != torch.int32 or k_lens.numel() < batch or k_lens.get_device() != device or not k_lens.is_contiguous():
         raise ValueError("k_lens holds one int32 a batch item on the current device")
-    return (_strided_arg("q1", q1, d.q_len, d.q_heads, d.d, d.q_stride, d, dev),
-            _strided_arg("q2", q2, d.q_len, d.q_heads, d.d, d.q_stride, d, dev),
-            _strided_arg("k1", k1, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev),
-            _strided_arg("k2", k2, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev),
-            _strided_arg("v", v, d.k_len, d.kv_heads, d.dv, d.v_stride, d, dev),
-            _arg("lam", lam, d.q_heads, d.lam_dtype, dev), None if k_lens is None else k_lens.data_ptr())
+    return k_lens.data_ptr()
 
 
 def rib_diff_attention_workspace_size(desc: DiffAttnDesc) -> int:
@@ -569,10 +584,10 @@ def rib_diff_attention(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens=None, 
     (None for inference) are what the backward needs (see include/rib.h)."""
     load()
     dev, d = _current_device(q1), desc
+    qa, ka, va, oa = _diff_args(d, dev)
     _check(_lib.rib_diff_attention(
-        ctypes.byref(d), *_diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev),
-        _strided_arg("o", o, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev),
-        _strided_arg("o2", o2, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev),
+        ctypes.byref(d), qa("q1", q1), qa("q2", q2), ka("k1", k1), ka("k2", k2), va("v", v), _arg("lam", lam, d.q_heads, d.lam_dtype, dev),
+        _lens_arg(k_lens, d.batch, dev), oa("o", o), oa("o2", o2),
         _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), *_workspace_arg(workspace, dev), _stream(stream)))
 
 
@@ -586,11 +601,9 @@ def rib_diff_attention_bwd(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens, o
     lse (see include/rib.h)."""
     load()
     dev, d = _current_device(q1), desc
-    out = [_strided_arg(n, t, d.q_len, d.q_heads, d.dv, d.o_stride, d, dev) for n, t in (("o", o), ("o2", o2), ("do", do))]
-    dq = [_strided_arg(n, t, d.q_len, d.q_heads, d.d, d.q_stride, d, dev) for n, t in (("dq1", dq1), ("dq2", dq2))]
-    dk = [_strided_arg(n, t, d.k_len, d.kv_heads, d.d, d.k_stride, d, dev) for n, t in (("dk1", dk1), ("dk2", dk2))]
+    qa, ka, va, oa = _diff_args(d, dev)
     _check(_lib.rib_diff_attention_bwd(
-        ctypes.byref(d), *_diff_inputs(d, q1, q2, k1, k2, v, lam, k_lens, dev), out[0], out[1],
-        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), out[2], *dq, *dk,
-        _strided_arg("dv", dv, d.k_len, d.kv_heads, d.dv, d.v_stride, d, dev), _arg("dlam", dlam, d.q_heads, d.lam_dtype, dev),
-        *_workspace_arg(workspace, dev), _stream(stream)))
+        ctypes.byref(d), qa("q1", q1), qa("q2", q2), ka("k1", k1), ka("k2", k2), va("v", v), _arg("lam", lam, d.q_heads, d.lam_dtype, dev),
+        _lens_arg(k_lens, d.batch, dev), oa("o", o), oa("o2", o2),
+        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), oa("do", do), qa("dq1", dq1), qa("dq2", dq2), ka("dk1", dk1),
+        ka("dk2", dk2), va("dv", dv), _arg("dlam", dlam, d.q_heads, d.lam_dtype, dev), *_workspace_arg(workspace, dev), _stream(stream)))
