@@ -12,7 +12,12 @@
 //   du = dx' f gate,  dpost_w = sum du y^,  dpost_b = sum du, dy from du post_w,
 //   dpre_w = sum dh x'^,  dpre_b = sum dh.
 //
-// What bounds both: memory. Each tensor is read or written once: a row lives
+// What bounds both: memory. Each tensor is read or written once. A CTA walks
+// blocks of whole rows, which are contiguous in every tensor: bulk copies
+// bring a block into shared memory while the block before is computed, results
+// overwrite their inputs there and leave by bulk copies, so no thread waits for
+// memory and odd widths move like even ones (blocks at a tensor's end, or of
+// tensors off a 16-byte boundary, are copied element by element). A row lives
 // in the registers of a group of `lpr` threads (a power of two from 4 to 512,
 // each thread NV vectors of V elements), statistics are two passes over those
 // registers (mean, then squared deviations: no cancellation), and the backward
@@ -59,11 +64,15 @@ struct NormParams {
   void *dx, *dy, *dgate;
   float* partial;           // [CTAs][kSums][C]
   int chunks;               // CTAs of a group
+  // blocks in shared memory: rows of one, the place of x, dx_out, y, gate and dh in a stage, bytes of a stage, stages
+  int block, off[5], stage_bytes, stages, bulk;
+  int* err;
 };
+enum { kX = 0, kD, kY, kG, kH };
 
 // V consecutive elements as fp32.
 template <typename T, int V>
-__device__ __forceinline__ void load_v(const void* base, size_t at, float (&f)[V]) {
+__device__ __forceinline__ void load_v(const void* base, uint32_t at, float (&f)[V]) {
   const T* p = static_cast<const T*>(base) + at;
   if constexpr (sizeof(T) == 4) {
     if constexpr (V == 4) {
@@ -86,10 +95,17 @@ __device__ __forceinline__ void load_v(const void* base, size_t at, float (&f)[V
     }
   }
 }
+// The same where `in`, else zeros.
+template <typename T, int V>
+__device__ __forceinline__ void load_if(const T* base, uint32_t at, bool in, float (&f)[V]) {
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = 0.f;
+  if (in) load_v<T, V>(base, at, f);
+}
 // SAT: fp16 results beyond +-65504 saturate, as in every forward store of the
 // library. Gradients do not: an overflow has to stay visible to loss scaling.
 template <typename T, int V, bool SAT>
-__device__ __forceinline__ void store_v(void* base, size_t at, const float (&f)[V]) {
+__device__ __forceinline__ void store_v(void* base, uint32_t at, const float (&f)[V]) {
   T* p = static_cast<T*>(base) + at;
   if constexpr (sizeof(T) == 4) {
     if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
@@ -122,20 +138,110 @@ __device__ __forceinline__ void row_sum(float (&v)[N], int lpr, float (*red)[2][
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
   if constexpr (WIDE) {
-    const int warp = threadIdx.x >> 5, per = lpr >> 5, first = warp / per * per;
-    if ((threadIdx.x & 31) == 0)
+    // the lanes of each warp read the row's warp sums (2 to 16 of them) and add them by shuffles
+    const int warp = threadIdx.x >> 5, per = lpr >> 5, lane = threadIdx.x & 31;
+    if (lane == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[phase][i][warp] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float s = 0.f;
-      for (int k = 0; k < per; ++k) s += red[phase][i][first + k];
-      v[i] = s;
-    }
+    for (int i = 0; i < N; ++i) v[i] = red[phase][i][(warp & ~(per - 1)) + (lane & (per - 1))];
+    for (int o = per >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(0xFFFFFFFFu, v[i], o);
     phase ^= 1;
   }
 }
+
+// Blocks of rows between memory and the stages of a CTA. Tensors that are
+// absent have null pointers.
+template <typename XT, typename YT>
+struct BlockIo {
+  const NormParams& p;
+  uint8_t* smem;
+  uint64_t* full;
+  volatile uint32_t* abort_flag;
+  uint32_t laps = 0u;   // a parity bit a stage
+
+  __device__ __forceinline__ int place(int t) const { return t == kX ? p.off[kX] : (t == kD ? p.off[kD] : (t == kY ? p.off[kY] : p.off[kG])); }
+  __device__ __forceinline__ bool whole(long long r0, long long r1) const { return p.bulk && r1 - r0 == p.block; }
+  // Thread 0: the stage's last results have left, then the next block comes in.
+  __device__ __forceinline__ void start(int st, long long r0, long long r1, const void* const (&src)[5]) const {
+    if (threadIdx.x != 0 || !whole(r0, r1)) return;
+    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    const uint32_t n = static_cast<uint32_t>(p.block) * p.C;
+    uint32_t bytes = 0;
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (src[i]) bytes += n * (i < kY ? sizeof(XT) : sizeof(YT));
+    mbar_arrive_expect_tx(&full[st], bytes);
+#pragma unroll
+    for (int i = 0; i < 5; ++i)
+      if (src[i]) {
+        const uint32_t size = i < kY ? sizeof(XT) : sizeof(YT);
+        bulk_load(smem + st * p.stage_bytes + p.off[i], static_cast<const uint8_t*>(src[i]) + static_cast<size_t>(r0) * p.C * size, n * size,
+                  &full[st]);
+      }
+  }
+  // All threads: the block is in its stage. False after a wait that ran out.
+  __device__ __forceinline__ bool ready(int st, long long r0, long long r1, const void* const (&src)[5]) {
+    bool ok = true;
+    if (whole(r0, r1)) {
+      ok = mbar_wait(&full[st], (laps >> st) & 1u, WaitCtx{abort_flag, p.err}, 501);
+      laps ^= 1u << st;
+    } else {
+      if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+      __syncthreads();
+      const size_t n = static_cast<size_t>(r1 - r0) * p.C, at = static_cast<size_t>(r0) * p.C;
+      uint8_t* to = smem + st * p.stage_bytes;
+#pragma unroll
+      for (int i = 0; i < 5; ++i) {
+        if (!src[i]) continue;
+        if (i < kY)
+          for (size_t e = threadIdx.x; e < n; e += blockDim.x) reinterpret_cast<XT*>(to + p.off[i])[e] = static_cast<const XT*>(src[i])[at + e];
+        else
+          for (size_t e = threadIdx.x; e < n; e += blockDim.x) reinterpret_cast<YT*>(to + p.off[i])[e] = static_cast<const YT*>(src[i])[at + e];
+      }
+    }
+    return __syncthreads_and(ok) != 0;
+  }
+  // All threads: results dst[k], held where tensor at[k] was, leave the stage.
+  __device__ __forceinline__ void finish(int st, long long r0, long long r1, void* const (&dst)[3], const int (&at)[3]) const {
+    const uint8_t* from = smem + st * p.stage_bytes;
+    if (whole(r0, r1)) {
+      fence_proxy_async_smem();
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        const uint32_t n = static_cast<uint32_t>(p.block) * p.C;
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+          if (dst[k]) {
+            const uint32_t size = at[k] < kY ? sizeof(XT) : sizeof(YT);
+            asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;"
+                         ::"l"(static_cast<uint8_t*>(dst[k]) + static_cast<size_t>(r0) * p.C * size), "r"(smem_u32(from + place(at[k]))),
+                           "r"(n * size) : "memory");
+          }
+        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+      }
+    } else {
+      __syncthreads();
+      const size_t n = static_cast<size_t>(r1 - r0) * p.C, to = static_cast<size_t>(r0) * p.C;
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        if (!dst[k]) continue;
+        if (at[k] < kY)
+          for (size_t e = threadIdx.x; e < n; e += blockDim.x) static_cast<XT*>(dst[k])[to + e] = reinterpret_cast<const XT*>(from + place(at[k]))[e];
+        else
+          for (size_t e = threadIdx.x; e < n; e += blockDim.x) static_cast<YT*>(dst[k])[to + e] = reinterpret_cast<const YT*>(from + place(at[k]))[e];
+      }
+      fence_proxy_async_smem();   // the stage's next block may come by bulk copies
+      __syncthreads();
+    }
+  }
+  __device__ __forceinline__ void drain() const {
+    if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+  }
+};
 
 // The dropout factor of V elements from flat element `at` (V == 4: at % 4 == 0).
 template <int V>
@@ -179,7 +285,7 @@ __device__ __forceinline__ float normalise(float (&v)[NV][V], const bool (&in)[N
 #pragma unroll
     for (int e = 0; e < V; ++e) s[0] = fmaf(v[k][e], v[k][e], s[0]);
   row_sum<1, WIDE>(s, lpr, red, phase);
-  const float r = 1.f / sqrtf(fmaf(s[0], p.inv_c, p.eps));
+  const float r = rsqrtf(fmaf(s[0], p.inv_c, p.eps));   // within 2 units in the last place
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -187,96 +293,150 @@ __device__ __forceinline__ float normalise(float (&v)[NV][V], const bool (&in)[N
   return r;
 }
 
+__device__ __forceinline__ long long group_of(long long row, long long per) {
+  if (((row | per) >> 32) == 0) return static_cast<uint32_t>(row) / static_cast<uint32_t>(per);
+  return row / per;
+}
+
 // One row per group of lpr threads, CTAs walking blocks of rows.
 template <typename XT, typename YT, int V, int NV, bool WIDE>
-__global__ void __launch_bounds__(512) residual_norm_fwd_kernel(const NormParams p, int lpr_log2) {
+__global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_constant__ NormParams p, int lpr_log2) {
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][2][32];
+  __shared__ uint64_t full[2];
+  __shared__ uint32_t abort_word;
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    abort_word = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
   int phase = 0;
   const int lpr = 1 << lpr_log2, lane = threadIdx.x & (lpr - 1), slot = threadIdx.x >> lpr_log2;
   const int rows_per_cta = blockDim.x >> lpr_log2;
   const uint64_t stream = p.rng.offset + (p.rng.threshold && p.rng.step ? *p.rng.step : 0ull);
-  const long long blocks = (p.T + rows_per_cta - 1) / rows_per_cta;
+  const long long blocks = (p.T + p.block - 1) / p.block;
+  BlockIo<XT, YT> io{p, smem, full, &abort_word};
+  const void* const src[5] = {p.x, nullptr, p.y, p.gate, nullptr};
+  void* const dst[3] = {p.y ? p.x_out : nullptr, p.pre ? p.h : nullptr, nullptr};
+  const int held[3] = {kX, kY, kY};
+  const auto last = [&](long long b) { return (b + 1) * p.block < p.T ? (b + 1) * p.block : p.T; };
+  if (blockIdx.x < blocks) io.start(0, static_cast<long long>(blockIdx.x) * p.block, last(blockIdx.x), src);
+  int st = 0;
+  // the weights of every column, in shared memory: post_w, post_b, pre_w, pre_b, scale (of the first group)
+  float* weights = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
+  const int wide_c = (p.C + 3) / 4 * 4;
+  for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+    weights[c] = p.post_w ? p.post_w[c] : 1.f;
+    weights[wide_c + c] = p.post_b ? p.post_b[c] : 0.f;
+    weights[2 * wide_c + c] = p.pre_w ? p.pre_w[c] : 1.f;
+    weights[3 * wide_c + c] = p.pre_b ? p.pre_b[c] : 0.f;
+    weights[4 * wide_c + c] = p.scale ? p.scale[c] : 1.f;
+  }
+  const bool many = p.scale && p.rows_per_group < p.T;   // groups
   for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
-    const long long row = b * rows_per_cta + slot;
-    const bool live = row < p.T;
-    const size_t base = live ? static_cast<size_t>(row) * p.C : 0;
-    bool in[NV];
-    float x[NV][V], u[NV][V], g[NV][V];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (lane + k * lpr) * V;
-      in[k] = live && c < p.C;
-#pragma unroll
-      for (int e = 0; e < V; ++e) x[k][e] = u[k][e] = 0.f, g[k][e] = 1.f;
-      if (in[k]) {
-        load_v<XT, V>(p.x, base + c, x[k]);
-        if (p.y) load_v<YT, V>(p.y, base + c, u[k]);
-        if (p.gate) load_v<YT, V>(p.gate, base + c, g[k]);
-      }
-    }
-    if (p.y) {
-      if (p.post) normalise<V, NV, WIDE>(u, in, p.post, p, lpr, red, phase);
-      const float* scale = p.scale ? p.scale + (live ? row / p.rows_per_group : 0) * p.C : nullptr;
+    const long long r0 = b * p.block, r1 = last(b), next = b + gridDim.x;
+    if (p.stages == 2 && next < blocks) io.start(st ^ 1, next * p.block, last(next), src);
+    if (!io.ready(st, r0, r1, src)) break;
+    uint8_t* stage = smem + st * p.stage_bytes;
+    for (int rr = slot; rr - slot < p.block; rr += rows_per_cta) {
+      const long long row = r0 + rr;
+      const bool live = row < r1;
+      const uint32_t at = (live ? rr * p.C : 0) + lane * V;
+      XT* sx = reinterpret_cast<XT*>(stage + p.off[kX]) + at;
+      YT* sy = reinterpret_cast<YT*>(stage + p.off[kY]) + at;
+      const YT* sg = reinterpret_cast<const YT*>(stage + p.off[kG]) + at;
+      bool in[NV];
+      float x[NV][V], u[NV][V];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (!in[k]) continue;
-        const int c = (lane + k * lpr) * V;
-        float a[V];
-        if (p.post_w) {
-          load_v<float, V>(p.post_w, c, a);
+        in[k] = live && (lane + k * lpr) * V < p.C;
+        load_if<XT, V>(sx, k * lpr * V, in[k], x[k]);
+      }
+      if (p.y) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) u[k][e] *= a[e];
+        for (int k = 0; k < NV; ++k) load_if<YT, V>(sy, k * lpr * V, in[k], u[k]);
+        if (p.post) normalise<V, NV, WIDE>(u, in, p.post, p, lpr, red, phase);
+        const float* w0 = weights + lane * V;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float w[V], c[V];
+          load_if<float, V>(w0, k * lpr * V, in[k], w);
+          load_if<float, V>(w0, wide_c + k * lpr * V, in[k], c);
+#pragma unroll
+          for (int e = 0; e < V; ++e) u[k][e] = fmaf(u[k][e], w[e], c[e]);
         }
-        if (p.post_b) {
-          load_v<float, V>(p.post_b, c, a);
+        const float* scale = many && live ? p.scale + group_of(row, p.rows_per_group) * p.C + lane * V : w0 + 4 * wide_c;
 #pragma unroll
-          for (int e = 0; e < V; ++e) u[k][e] += a[e];
+        for (int k = 0; k < NV; ++k) {
+          float w[V];
+          load_if<float, V>(scale, k * lpr * V, in[k], w);
+#pragma unroll
+          for (int e = 0; e < V; ++e) u[k][e] *= w[e];
         }
-        if (scale) {
-          load_v<float, V>(scale, c, a);
+        if (p.gate) {
 #pragma unroll
-          for (int e = 0; e < V; ++e) g[k][e] *= a[e];
+          for (int k = 0; k < NV; ++k) {
+            float g[V];
+            load_if<YT, V>(sg, k * lpr * V, in[k], g);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[k][e] *= g[e];
+          }
         }
         if (p.rng.threshold) {
-          // a dropped element adds 0 whatever the branch holds
-          drop_factor<V>(p.rng, stream, base + c, a);
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] += a[e] != 0.f ? a[e] * g[k][e] * u[k][e] : 0.f;
-        } else {
+          for (int k = 0; k < NV; ++k) {
+            float m[V];
+            drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V, m);
+            // a dropped element adds 0 whatever the branch holds
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] = fmaf(g[k][e], u[k][e], x[k][e]);
+            for (int e = 0; e < V; ++e) u[k][e] = m[e] != 0.f ? m[e] * u[k][e] : 0.f;
+          }
         }
-        if (p.x_out) store_v<XT, V, true>(p.x_out, base + c, x[k]);
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[k][e] = in[k] ? x[k][e] + u[k][e] : 0.f;
+        if (p.x_out)
+#pragma unroll
+          for (int k = 0; k < NV; ++k)
+            if (in[k]) store_v<XT, V, true>(sx, k * lpr * V, x[k]);
+      }
+      if (p.pre) {
+        normalise<V, NV, WIDE>(x, in, p.pre, p, lpr, red, phase);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float w[V], c[V];
+          load_if<float, V>(weights + lane * V, 2 * wide_c + k * lpr * V, in[k], w);
+          load_if<float, V>(weights + lane * V, 3 * wide_c + k * lpr * V, in[k], c);
+#pragma unroll
+          for (int e = 0; e < V; ++e) x[k][e] = fmaf(x[k][e], w[e], c[e]);
+          if (in[k]) store_v<YT, V, true>(sy, k * lpr * V, x[k]);
+        }
       }
     }
-    if (p.pre) {
-      normalise<V, NV, WIDE>(x, in, p.pre, p, lpr, red, phase);
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        if (!in[k]) continue;
-        const int c = (lane + k * lpr) * V;
-        float a[V];
-        if (p.pre_w) {
-          load_v<float, V>(p.pre_w, c, a);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] *= a[e];
-        }
-        if (p.pre_b) {
-          load_v<float, V>(p.pre_b, c, a);
-#pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] += a[e];
-        }
-        store_v<YT, V, true>(p.h, base + c, x[k]);
-      }
-    }
+    io.finish(st, r0, r1, dst, held);
+    if (p.stages == 2) st ^= 1;
+    else if (next < blocks) io.start(0, next * p.block, last(next), src);
   }
+  io.drain();
 }
 
 // CTA (group, chunk): rows of one scale group, so dscale's partials never mix groups.
 template <typename XT, typename YT, int V, int NV, bool WIDE>
-__global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const NormParams p, int lpr_log2) {
-  extern __shared__ float acc_smem[];   // [slots][lpr * NV * V], one sum at a time
+__global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_constant__ NormParams p, int lpr_log2) {
+  extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float red[2][2][32];
+  __shared__ uint64_t full[2];
+  __shared__ uint32_t abort_word;
+  if (threadIdx.x == 0) {
+    mbar_init(&full[0], 1);
+    mbar_init(&full[1], 1);
+    abort_word = 0u;
+    fence_barrier_init();
+  }
+  __syncthreads();
   int phase = 0;
   const int lpr = 1 << lpr_log2, lane = threadIdx.x & (lpr - 1), slot = threadIdx.x >> lpr_log2;
   const int rows_per_cta = blockDim.x >> lpr_log2;
@@ -293,108 +453,141 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const NormParams
 #pragma unroll
       for (int e = 0; e < V; ++e) acc[s][k][e] = 0.f;
 
-  // every thread of the CTA takes the same number of steps (the row sums meet at barriers)
-  for (long long r0 = g0 + chunk * rows_per_cta; r0 < g1; r0 += static_cast<long long>(p.chunks) * rows_per_cta) {
-    const long long row = r0 + slot;
-    const bool live = row < g1;
-    const size_t base = live ? static_cast<size_t>(row) * p.C : 0;
-    bool in[NV];
-    float xh[NV][V], u[NV][V], g[NV][V], d[NV][V], dh[NV][V];
+  // this chunk's share of the group's blocks, which lie at multiples of p.block of all rows
+  const long long b0 = g0 / p.block, n_blocks = g1 > g0 ? (g1 - 1) / p.block - b0 + 1 : 0;
+  const long long first = b0 + n_blocks * chunk / p.chunks, behind = b0 + n_blocks * (chunk + 1) / p.chunks;
+  BlockIo<XT, YT> io{p, smem, full, &abort_word};
+  const bool pre = p.pre != 0;
+  const void* const src[5] = {pre ? p.x : nullptr, p.dx_out, p.y, p.gate, pre ? p.dh : nullptr};
+  const int dx_at = pre ? kX : kD;
+  void* const dst[3] = {p.dx, p.y ? p.dy : nullptr, p.y ? p.dgate : nullptr};
+  const int held[3] = {dx_at, kY, kG};
+  const auto lo = [&](long long b) { return b * p.block > g0 ? b * p.block : g0; };
+  const auto hi = [&](long long b) { return (b + 1) * p.block < g1 ? (b + 1) * p.block : g1; };
+  if (first < behind) io.start(0, lo(first), hi(first), src);
+  // the weights of every column, in shared memory: pre_w, post_w, post_b, scale
+  float* weights = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
+  const int wide_c = (p.C + 3) / 4 * 4;
+  for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
+    weights[c] = p.pre_w ? p.pre_w[c] : 1.f;
+    weights[wide_c + c] = p.post_w ? p.post_w[c] : 1.f;
+    weights[2 * wide_c + c] = p.post_b ? p.post_b[c] : 0.f;
+    weights[3 * wide_c + c] = scale ? scale[c] : 1.f;
+  }
+  int st = 0;
+  for (long long blk = first; blk < behind; ++blk) {
+    const long long r0 = lo(blk), r1 = hi(blk);
+    if (p.stages == 2 && blk + 1 < behind) io.start(st ^ 1, lo(blk + 1), hi(blk + 1), src);
+    if (!io.ready(st, r0, r1, src)) break;
+    uint8_t* stage = smem + st * p.stage_bytes;
+    // every thread of the CTA takes the same number of steps (the row sums meet at barriers)
+    for (int rr = slot; rr - slot < p.block; rr += rows_per_cta) {
+      const long long row = r0 + rr;
+      const bool live = row < r1;
+      const uint32_t at = (live ? rr * p.C : 0) + lane * V;
+      XT* sx = reinterpret_cast<XT*>(stage + p.off[kX]) + at;
+      XT* sd = reinterpret_cast<XT*>(stage + p.off[kD]) + at;
+      YT* sy = reinterpret_cast<YT*>(stage + p.off[kY]) + at;
+      YT* sg = reinterpret_cast<YT*>(stage + p.off[kG]) + at;
+      const YT* sh = reinterpret_cast<const YT*>(stage + p.off[kH]) + at;
+      const float* w0 = weights + lane * V;
+      bool in[NV];
+      float d[NV][V];
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (lane + k * lpr) * V;
-      in[k] = live && c < p.C;
-#pragma unroll
-      for (int e = 0; e < V; ++e) xh[k][e] = u[k][e] = d[k][e] = dh[k][e] = 0.f, g[k][e] = 1.f;
-      if (in[k]) {
-        if (p.pre) {
-          load_v<XT, V>(p.x, base + c, xh[k]);
-          load_v<YT, V>(p.dh, base + c, dh[k]);
-        }
-        if (p.y) load_v<YT, V>(p.y, base + c, u[k]);
-        if (p.gate) load_v<YT, V>(p.gate, base + c, g[k]);
-        if (p.dx_out) load_v<XT, V>(p.dx_out, base + c, d[k]);
+      for (int k = 0; k < NV; ++k) {
+        in[k] = live && (lane + k * lpr) * V < p.C;
+        load_if<XT, V>(sd, k * lpr * V, in[k] && p.dx_out, d[k]);
       }
-    }
-    if (p.pre) {
-      const float r = normalise<V, NV, WIDE>(xh, in, p.pre, p, lpr, red, phase);
+      if (pre) {
+        float xh[NV][V], dh[NV][V];
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          load_if<XT, V>(sx, k * lpr * V, in[k], xh[k]);
+          load_if<YT, V>(sh, k * lpr * V, in[k], dh[k]);
+        }
+        const float r = normalise<V, NV, WIDE>(xh, in, p.pre, p, lpr, red, phase);
+        float s[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float w[V];
+          load_if<float, V>(w0, k * lpr * V, in[k], w);
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            acc[3][k][e] = fmaf(dh[k][e], xh[k][e], acc[3][k][e]);
+            acc[4][k][e] += dh[k][e];
+            dh[k][e] *= w[e];
+            s[0] += dh[k][e];
+            s[1] = fmaf(dh[k][e], xh[k][e], s[1]);
+          }
+        }
+        row_sum<2, WIDE>(s, lpr, red, phase);
+        const float m0 = p.pre == 1 ? s[0] * p.inv_c : 0.f, m1 = s[1] * p.inv_c;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int e = 0; e < V; ++e) d[k][e] = in[k] ? fmaf(r, dh[k][e] - m0 - xh[k][e] * m1, d[k][e]) : 0.f;
+      }
+      if (p.dx) {
+        XT* out = pre ? sx : sd;
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+          if (in[k]) store_v<XT, V, false>(out, k * lpr * V, d[k]);
+      }
+      if (!p.y) continue;
+      float u[NV][V];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) load_if<YT, V>(sy, k * lpr * V, in[k], u[k]);
+      float ry = 1.f;
+      if (p.post) ry = normalise<V, NV, WIDE>(u, in, p.post, p, lpr, red, phase);
       float s[2] = {0.f, 0.f};
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int c = (lane + k * lpr) * V;
-        float w[V];
+        float w[V], b[V], sc[V], m[V], g[V], dg[V];
+        load_if<float, V>(w0, wide_c + k * lpr * V, in[k], w);
+        load_if<float, V>(w0, 2 * wide_c + k * lpr * V, in[k], b);
+        load_if<float, V>(w0, 3 * wide_c + k * lpr * V, in[k], sc);
 #pragma unroll
-        for (int e = 0; e < V; ++e) w[e] = 1.f;
-        if (in[k] && p.pre_w) load_v<float, V>(p.pre_w, c, w);
+        for (int e = 0; e < V; ++e) m[e] = g[e] = 1.f;
+        if (p.gate) load_if<YT, V>(sg, k * lpr * V, in[k], g);
+        if (p.rng.threshold) drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V, m);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          acc[3][k][e] = fmaf(dh[k][e], xh[k][e], acc[3][k][e]);
-          acc[4][k][e] += dh[k][e];
-          dh[k][e] *= w[e];
-          s[0] += dh[k][e];
-          s[1] = fmaf(dh[k][e], xh[k][e], s[1]);
+          const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
+          const float dm = m[e] != 0.f ? d[k][e] * m[e] : 0.f;
+          const float dmu = m[e] != 0.f ? dm * uu : 0.f;
+          dg[e] = dmu * sc[e];
+          acc[0][k][e] = fmaf(dmu, g[e], acc[0][k][e]);
+          const float du = dm * sc[e] * g[e];
+          acc[1][k][e] = fmaf(du, u[k][e], acc[1][k][e]);
+          acc[2][k][e] += du;
+          d[k][e] = du * w[e];
+          s[0] += d[k][e];
+          s[1] = fmaf(d[k][e], u[k][e], s[1]);
         }
+        if (in[k] && p.dgate) store_v<YT, V, false>(sg, k * lpr * V, dg);
       }
-      row_sum<2, WIDE>(s, lpr, red, phase);
-      const float m0 = p.pre == 1 ? s[0] * p.inv_c : 0.f, m1 = s[1] * p.inv_c;
+      if (!p.dy) continue;
+      if (p.post) {
+        row_sum<2, WIDE>(s, lpr, red, phase);
+        const float m0 = p.post == 1 ? s[0] * p.inv_c : 0.f, m1 = s[1] * p.inv_c;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
+        for (int k = 0; k < NV; ++k)
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[k][e] = in[k] ? fmaf(r, dh[k][e] - m0 - xh[k][e] * m1, d[k][e]) : 0.f;
-    }
-    if (p.dx)
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (in[k]) store_v<XT, V, false>(p.dx, base + (lane + k * lpr) * V, d[k]);
-    if (!p.y) continue;
-    float ry = 1.f;
-    if (p.post) ry = normalise<V, NV, WIDE>(u, in, p.post, p, lpr, red, phase);
-    float s[2] = {0.f, 0.f};
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int c = (lane + k * lpr) * V;
-      float w[V], b[V], sc[V], m[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) w[e] = sc[e] = m[e] = 1.f, b[e] = 0.f;
-      if (in[k]) {
-        if (p.post_w) load_v<float, V>(p.post_w, c, w);
-        if (p.post_b) load_v<float, V>(p.post_b, c, b);
-        if (scale) load_v<float, V>(scale, c, sc);
-        if (p.rng.threshold) drop_factor<V>(p.rng, stream, base + c, m);
+          for (int e = 0; e < V; ++e) d[k][e] = ry * (d[k][e] - m0 - u[k][e] * m1);
       }
-      float dg[V];
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
-        const float dm = m[e] != 0.f ? d[k][e] * m[e] : 0.f;
-        const float dmu = m[e] != 0.f ? dm * uu : 0.f;
-        dg[e] = dmu * sc[e];
-        acc[0][k][e] = fmaf(dmu, g[k][e], acc[0][k][e]);
-        const float du = dm * sc[e] * g[k][e];
-        acc[1][k][e] = fmaf(du, u[k][e], acc[1][k][e]);
-        acc[2][k][e] += du;
-        d[k][e] = du * w[e];
-        s[0] += d[k][e];
-        s[1] = fmaf(d[k][e], u[k][e], s[1]);
-      }
-      if (in[k] && p.dgate) store_v<YT, V, false>(p.dgate, base + c, dg);
-    }
-    if (p.post) {
-      row_sum<2, WIDE>(s, lpr, red, phase);
-      const float m0 = p.post == 1 ? s[0] * p.inv_c : 0.f, m1 = s[1] * p.inv_c;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-#pragma unroll
-        for (int e = 0; e < V; ++e) d[k][e] = ry * (d[k][e] - m0 - u[k][e] * m1);
+        if (in[k]) store_v<YT, V, false>(sy, k * lpr * V, d[k]);
     }
-    if (p.dy)
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (in[k]) store_v<YT, V, false>(p.dy, base + (lane + k * lpr) * V, d[k]);
+    io.finish(st, r0, r1, dst, held);
+    if (p.stages == 2) st ^= 1;
+    else if (blk + 1 < behind) io.start(0, lo(blk + 1), hi(blk + 1), src);
   }
+  io.drain();
 
   // the CTA's groups of threads, one sum at a time, in their order
   if (!p.partial) return;
+  float* acc_smem = reinterpret_cast<float*>(smem);   // [slots][lpr * NV * V], one sum at a time
   const int width = lpr * NV * V;
 #pragma unroll
   for (int s = 0; s < kSums; ++s) {
@@ -465,51 +658,105 @@ RowShape row_shape(int C, bool vec, int max_nv) {
   return best;
 }
 
-int cta_threads(int lpr_log2) { return lpr_log2 > 8 ? 512 : 256; }
+// Threads of a CTA: 512 for rows of 512 threads, and where a block's shared
+// memory leaves room for no more than two CTAs an SM.
+int cta_threads(int lpr_log2, long long block_bytes) { return lpr_log2 > 8 || block_bytes > 56 * 1024 ? 512 : 256; }
+// Rows that make whole 16-byte pieces of a tensor of that element size.
+int row_unit(int C, int size) {
+  int unit = 1;
+  while (unit < 8 && static_cast<long long>(unit) * C * size % 16) unit *= 2;
+  return unit;
+}
 
-long long bwd_chunks(long long T, long long rows_per_group, int groups, int rows_per_cta) {
-  // two CTAs an SM over all groups, no more than a group has blocks of rows
-  const long long target = 2ll * 148;
-  long long chunks = (target + groups - 1) / groups;
+// CTAs of a group in the backward: two an SM over all groups, no more than the group has rows.
+long long bwd_chunks(long long T, long long rows_per_group, int groups) {
+  const long long chunks = (2ll * 148 + groups - 1) / groups;
   const long long rows = rows_per_group < T ? rows_per_group : T;
-  const long long blocks = (rows + rows_per_cta - 1) / rows_per_cta;
-  return chunks < blocks ? (chunks > 0 ? chunks : 1) : (blocks > 0 ? blocks : 1);
+  return chunks < rows ? chunks : (rows > 0 ? rows : 1);
+}
+
+// Rows of a block and its place in shared memory. Bulk copies need whole
+// multiples of 16 bytes, that is 8 / gcd(C, 8) rows of a 16-bit tensor. Blocks
+// of about 24 KB in two stages leave room for two to four CTAs an SM; wide
+// rows get what fits, in one stage.
+constexpr int kSmemMost = 224 * 1024;
+void plan_blocks(NormParams* p, const void* const (&src)[5], const bool (&held)[5], int xs, int ys, int rows_per_cta, bool aligned, int extra) {
+  int elem = 0;
+  for (int i = 0; i < 5; ++i)
+    if (src[i] || held[i]) elem += i < kY ? xs : ys;
+  const int unit = row_unit(p->C, ys);
+  const auto bytes = [&](int rows) {   // each tensor's part on a 16-byte boundary
+    int n = 0;
+    for (int i = 0; i < 5; ++i) {
+      p->off[i] = n;
+      if (src[i] || held[i]) n += (rows * p->C * (i < kY ? xs : ys) + 127) / 128 * 128;
+    }
+    return n;
+  };
+  int rows = rows_per_cta > unit ? rows_per_cta : unit;
+  p->bulk = aligned && bytes(rows) + extra <= kSmemMost;
+  if (!p->bulk) rows = rows_per_cta;
+  while (static_cast<long long>(rows) * p->C * elem < 16 * 1024 && rows < 512) rows *= 2;
+  p->block = rows;
+  p->stage_bytes = bytes(rows);
+  p->stages = p->bulk && 2 * p->stage_bytes + extra <= kSmemMost / 2 ? 2 : 1;
+}
+
+// Beyond 48 KB, static arrays included, a kernel has to ask.
+template <typename K>
+cudaError_t allow_smem(K kernel, int bytes) {
+  return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
 }
 
 template <typename XT, typename YT>
-cudaError_t launch_fwd(const NormParams& p, bool vec, cudaStream_t stream) {
+cudaError_t launch_fwd(NormParams p, bool vec, bool aligned, cudaStream_t stream) {
   const RowShape s = row_shape(p.C, vec, 3);
-  const int threads = cta_threads(s.lpr_log2), rows_per_cta = threads >> s.lpr_log2;
-  const long long blocks = (p.T + rows_per_cta - 1) / rows_per_cta;
-  const long long most = static_cast<long long>(sm_count()) * (2048 / threads);
+  const int threads = cta_threads(s.lpr_log2, static_cast<long long>(row_unit(p.C, sizeof(YT))) * p.C * (sizeof(XT) + 2 * sizeof(YT)));
+  const int rows_per_cta = threads >> s.lpr_log2;
+  plan_blocks(&p, {p.x, nullptr, p.y, p.gate, nullptr}, {true, false, true, false, false}, sizeof(XT), sizeof(YT), rows_per_cta, aligned, 20 * p.C + 80);
+  const int smem = p.stages * p.stage_bytes + 20 * ((p.C + 3) / 4 * 4);
+  const long long blocks = (p.T + p.block - 1) / p.block;
+  const int by_smem = 227 * 1024 / (smem + 2048), by_threads = 1024 / threads;
+  const long long most = static_cast<long long>(sm_count()) * (by_smem < by_threads ? by_smem : by_threads);
   const unsigned grid = static_cast<unsigned>(blocks < most ? blocks : most);
   const bool wide = s.lpr_log2 > 5;
-#define RIB_FWD(V, NV)                                                                                              \
-  if (s.v == V && s.nv == NV) {                                                                                     \
-    if (wide) residual_norm_fwd_kernel<XT, YT, V, NV, true><<<grid, threads, 0, stream>>>(p, s.lpr_log2);           \
-    else residual_norm_fwd_kernel<XT, YT, V, NV, false><<<grid, threads, 0, stream>>>(p, s.lpr_log2);               \
-    return cudaGetLastError();                                                                                      \
-  }
+  const auto run = [&](auto kernel) {
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, threads, smem, stream>>>(p, s.lpr_log2);
+    return cudaGetLastError();
+  };
+#define RIB_FWD(V, NV)                                                                     \
+  if (s.v == V && s.nv == NV) return wide ? run(residual_norm_fwd_kernel<XT, YT, V, NV, true>) \
+                                          : run(residual_norm_fwd_kernel<XT, YT, V, NV, false>);
   RIB_FWD(4, 1) RIB_FWD(4, 2) RIB_FWD(4, 3) RIB_FWD(1, 4) RIB_FWD(1, 8)
 #undef RIB_FWD
   return cudaErrorInvalidConfiguration;
 }
 
 template <typename XT, typename YT>
-cudaError_t launch_bwd(NormParams p, bool vec, int groups, cudaStream_t stream) {
-  const RowShape s = row_shape(p.C, vec, 2);
-  const int threads = cta_threads(s.lpr_log2), rows_per_cta = threads >> s.lpr_log2;
-  p.chunks = static_cast<int>(bwd_chunks(p.T, p.rows_per_group, groups, rows_per_cta));
+cudaError_t launch_bwd(NormParams p, bool vec, bool aligned, int groups, cudaStream_t stream) {
+  const RowShape s = row_shape(p.C, vec, 3);
+  const int threads = cta_threads(s.lpr_log2, static_cast<long long>(row_unit(p.C, sizeof(YT))) * p.C * (2 * sizeof(XT) + 3 * sizeof(YT)));
+  const int rows_per_cta = threads >> s.lpr_log2;
+  const bool pre = p.pre != 0;
+  plan_blocks(&p, {pre ? p.x : nullptr, p.dx_out, p.y, p.gate, pre ? p.dh : nullptr}, {false, false, false, false, false}, sizeof(XT),
+              sizeof(YT), rows_per_cta, aligned, 16 * p.C + 64);
+  p.chunks = static_cast<int>(bwd_chunks(p.T, p.rows_per_group, groups));
   const unsigned grid = static_cast<unsigned>(p.chunks) * groups;
-  const size_t smem = p.partial ? static_cast<size_t>(rows_per_cta) * (s.v * s.nv << s.lpr_log2) * sizeof(float) : 0;
+  const int sums = p.partial ? rows_per_cta * (s.v * s.nv << s.lpr_log2) * static_cast<int>(sizeof(float)) : 0;
+  const int stages = p.stages * p.stage_bytes + 16 * ((p.C + 3) / 4 * 4), smem = stages > sums ? stages : sums;
   const bool wide = s.lpr_log2 > 5;
-#define RIB_BWD(V, NV)                                                                                              \
-  if (s.v == V && s.nv == NV) {                                                                                     \
-    if (wide) residual_norm_bwd_kernel<XT, YT, V, NV, true><<<grid, threads, smem, stream>>>(p, s.lpr_log2);        \
-    else residual_norm_bwd_kernel<XT, YT, V, NV, false><<<grid, threads, smem, stream>>>(p, s.lpr_log2);            \
-    return cudaGetLastError();                                                                                      \
-  }
-  RIB_BWD(4, 1) RIB_BWD(4, 2) RIB_BWD(1, 4) RIB_BWD(1, 8)
+  const auto run = [&](auto kernel) {
+    const cudaError_t e = allow_smem(kernel, smem);
+    if (e != cudaSuccess) return e;
+    kernel<<<grid, threads, smem, stream>>>(p, s.lpr_log2);
+    return cudaGetLastError();
+  };
+#define RIB_BWD(V, NV)                                                                     \
+  if (s.v == V && s.nv == NV) return wide ? run(residual_norm_bwd_kernel<XT, YT, V, NV, true>) \
+                                          : run(residual_norm_bwd_kernel<XT, YT, V, NV, false>);
+  RIB_BWD(4, 1) RIB_BWD(4, 2) RIB_BWD(4, 3) RIB_BWD(1, 4) RIB_BWD(1, 8)
 #undef RIB_BWD
   return cudaErrorInvalidConfiguration;
 }
@@ -543,11 +790,12 @@ int group_count(const rib_residual_norm_desc* d) {
 
 // Vectors of four need C % 4 == 0 and every tensor on a vector's boundary.
 struct Aligner {
-  bool vec = true, element = true;
+  bool vec = true, element = true, bulk = true;   // bulk: 16 bytes
   void add(const void* p, int dtype) {
     const uintptr_t size = dtype == RIB_F32 ? 4 : 2, a = reinterpret_cast<uintptr_t>(p);
     if (a % size) element = false;
     if (a % (4 * size)) vec = false;
+    if (a % 16) bulk = false;
   }
 };
 
@@ -577,6 +825,7 @@ rib_status rib_residual_norm(const rib_residual_norm_desc* d, const void* x, con
   a.add(x, d->x_dtype);
   a.add(x_out, d->x_dtype);
   for (const void* q : {y, gate, static_cast<const void*>(h)}) a.add(q, d->dtype);
+  const Aligner t = a;   // the tensors that move in blocks
   for (const float* q : {scale, post_w, post_b, pre_w, pre_b}) a.add(q, RIB_F32);
   if (!a.element || reinterpret_cast<uintptr_t>(step) % 8) return bad(who, RIB_ERR_ALIGNMENT, "tensors need their element's alignment, step 8 bytes");
   NormParams p{};
@@ -584,14 +833,15 @@ rib_status rib_residual_norm(const rib_residual_norm_desc* d, const void* x, con
   p.eps = d->eps; p.inv_c = 1.f / d->C;
   p.x = x; p.y = y; p.gate = gate; p.scale = scale; p.post_w = post_w; p.post_b = post_b; p.pre_w = pre_w; p.pre_b = pre_b;
   p.x_out = x_out; p.h = h;
+  if (!(p.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
   make_drop_rng(d->p, d->seed, d->offset, step, &p.rng);
   const bool vec = a.vec && d->C % 4 == 0;
   cudaError_t e;
-  if (d->x_dtype == RIB_BF16) e = launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, stream);
-  else if (d->x_dtype == RIB_F16) e = launch_fwd<__half, __half>(p, vec, stream);
-  else if (d->dtype == RIB_BF16) e = launch_fwd<float, __nv_bfloat16>(p, vec, stream);
-  else if (d->dtype == RIB_F16) e = launch_fwd<float, __half>(p, vec, stream);
-  else e = launch_fwd<float, float>(p, vec, stream);
+  if (d->x_dtype == RIB_BF16) e = launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, stream);
+  else if (d->x_dtype == RIB_F16) e = launch_fwd<__half, __half>(p, vec, t.bulk, stream);
+  else if (d->dtype == RIB_BF16) e = launch_fwd<float, __nv_bfloat16>(p, vec, t.bulk, stream);
+  else if (d->dtype == RIB_F16) e = launch_fwd<float, __half>(p, vec, t.bulk, stream);
+  else e = launch_fwd<float, float>(p, vec, t.bulk, stream);
   if (e != cudaSuccess) return cuda_fail(e, "rib_residual_norm launch");
   return RIB_OK;
 }
@@ -599,16 +849,7 @@ rib_status rib_residual_norm(const rib_residual_norm_desc* d, const void* x, con
 size_t rib_residual_norm_bwd_workspace_size(const rib_residual_norm_desc* d) {
   if (!d || d->T <= 0 || d->C <= 0 || d->C > kMaxC || d->rows_per_group <= 0) return 0;
   const int groups = group_count(d);
-  // the vector and the scalar form take different rows a CTA: the larger of the two
-  size_t most = 0;
-  for (int vec = 0; vec < 2; ++vec) {
-    if (vec && d->C % 4) continue;
-    const RowShape s = row_shape(d->C, vec, 2);
-    const int rows_per_cta = cta_threads(s.lpr_log2) >> s.lpr_log2;
-    const size_t n = static_cast<size_t>(bwd_chunks(d->T, d->rows_per_group, groups, rows_per_cta)) * groups;
-    most = n > most ? n : most;
-  }
-  return most * kSums * d->C * sizeof(float);
+  return static_cast<size_t>(bwd_chunks(d->T, d->rows_per_group, groups)) * groups * kSums * d->C * sizeof(float);
 }
 
 rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_out, const void* y, const void* gate,
@@ -639,6 +880,7 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_
   a.add(dx_out, d->x_dtype);
   a.add(dx, d->x_dtype);
   for (const void* q : {y, gate, dh, static_cast<const void*>(dy), static_cast<const void*>(dgate)}) a.add(q, d->dtype);
+  const Aligner t = a;   // the tensors that move in blocks
   for (const float* q : {scale, post_w, post_b, pre_w}) a.add(q, RIB_F32);
   Aligner b;   // written one element at a time
   for (const float* q : {dscale, dpost_w, dpost_b, dpre_w, dpre_b}) b.add(q, RIB_F32);
@@ -656,16 +898,16 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_
     p.x = x_out; p.y = y; p.gate = gate; p.scale = scale; p.post_w = post_w; p.post_b = post_b; p.pre_w = pre_w;
     p.dx_out = dx_out; p.dh = dh; p.dx = dx; p.dy = dy; p.dgate = dgate;
     p.partial = sums ? static_cast<float*>(ws) : nullptr;
+    if (!(p.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
     make_drop_rng(d->p, d->seed, d->offset, step, &p.rng);
     const bool vec = a.vec && d->C % 4 == 0;
-    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, groups, stream);
-    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, groups, stream);
-    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, groups, stream);
-    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, groups, stream);
-    else e = launch_bwd<float, float>(p, vec, groups, stream);
+    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, groups, stream);
+    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, t.bulk, groups, stream);
+    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, t.bulk, groups, stream);
+    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, t.bulk, groups, stream);
+    else e = launch_bwd<float, float>(p, vec, t.bulk, groups, stream);
     if (e != cudaSuccess) return cuda_fail(e, "rib_residual_norm_bwd launch");
-    const RowShape s = row_shape(d->C, vec, 2);
-    sp.chunks = static_cast<int>(bwd_chunks(d->T, d->rows_per_group, groups, cta_threads(s.lpr_log2) >> s.lpr_log2));
+    sp.chunks = static_cast<int>(bwd_chunks(d->T, d->rows_per_group, groups));
   }
   if (!sums) return RIB_OK;
   // no rows: the sums are empty and the gradients zero

@@ -91,6 +91,7 @@ const char* site_name(int s) {
     case 426: return "differential attention backward: dS written";
     case 427: return "differential attention backward: accumulate MMAs";
     case 428: return "differential attention backward: MMA drain";
+    case 501: return "residual norm: block loaded";
     case 901: return "self-test wait (nothing arrives)";
     default: return "unknown";
   }
