@@ -181,9 +181,9 @@ def test_diff_attention_argument_refusals(lib):
 
 
 def test_diff_attention_workspace_sizes(lib):
-    # six arrays of 32-bit row constants, rows of a key head padded to 128
-    assert rib.rib_diff_attention_bwd_workspace_size(_attn()._obj) == 2 * 2 * 256 * 6 * 4
-    assert rib.rib_diff_attention_bwd_workspace_size(_attn(q_len=70, k_len=70, window=8, width=10)._obj) == 2 * 2 * 2 * 128 * 6 * 4
+    # 60 bytes a row of row constants, 64 rows a box, an even number of boxes a key head; two cells of 8x7 and 2x7 tokens an item
+    assert rib.rib_diff_attention_bwd_workspace_size(_attn()._obj) == 2 * 2 * 4 * 64 * 60
+    assert rib.rib_diff_attention_bwd_workspace_size(_attn(q_len=70, k_len=70, window=8, width=10)._obj) == 2 * 2 * 2 * 2 * 64 * 60
     assert rib.rib_diff_attention_workspace_size(_attn()._obj) == 0
     for kw in ({"batch": 0}, {"q_len": 0}, {"k_len": 0}):
         assert rib.rib_diff_attention_workspace_size(_attn(**kw)._obj) == 0

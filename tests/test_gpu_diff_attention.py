@@ -227,6 +227,14 @@ def test_long_sequences(cuda_lib):
     _check(cuda_lib, 1, 6000, 6000, 1, 1, 16, 32, F16, rms=ALL)
 
 
+@pytest.mark.parametrize("t", [BF16, F16])
+def test_split_key_sums(cuda_lib, t):
+    """Few key tiles over many rows: their sums are split and added, empty shares and keys behind a length among them."""
+    _check(cuda_lib, 1, 3000, 200, 2, 1, 32, 64, t, rms=ALL)
+    _check(cuda_lib, 2, 1500, 300, 4, 2, 16, 32, t, lens=[300, 129])
+    _check(cuda_lib, 1, 2100, 2100, 8, 1, 64, 128, t, causal=True, rms=ALL)
+
+
 def test_lambda_in_fp32(cuda_lib):
     _check(cuda_lib, 1, 100, 100, 4, 2, 16, 32, BF16, lam_t=F32)
 

@@ -141,7 +141,7 @@ uintptr_t lam_size(const rib_diff_attn_desc* d) { return d->lam_dtype == RIB_F32
 // Query boxes of one (sequence, key head) in the backward's row constants: whole tiles of two.
 int row_boxes(const DiffGeom& g) { return ceil_div(diff_max_q_boxes(g), 2) * 2; }
 size_t row_bytes(const DiffGeom& g) {
-  return static_cast<size_t>(diff_sequences(g)) * g.kv_heads * row_boxes(g) * kRowArrays * 64 * sizeof(float);
+  return static_cast<size_t>(diff_sequences(g)) * g.kv_heads * row_boxes(g) * DiffRows::kBytes;
 }
 
 }  // namespace
@@ -185,7 +185,7 @@ rib_status rib_diff_attention(const rib_diff_attn_desc* d, const void* q1, const
 
 size_t rib_diff_attention_bwd_workspace_size(const rib_diff_attn_desc* d) {
   DiffGeom g;
-  return geometry("rib_diff_attention_bwd_workspace_size", d, &g) == RIB_OK ? row_bytes(g) : 0;
+  return geometry("rib_diff_attention_bwd_workspace_size", d, &g) == RIB_OK ? row_bytes(g) + diff_bwd_part_bytes(g) : 0;
 }
 
 rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, const void* q2, const void* k1, const void* k2, const void* v,
@@ -209,8 +209,10 @@ rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, c
       overlaps(g.v, d->batch, d->k_len, d->kv_heads, d->dv))
     return bad(who, RIB_ERR_INVALID_ARG, "strides lay gradients on one another");
   a.boxes = row_boxes(g);
-  if (rows && (!ws || ws_bytes < row_bytes(g))) return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
-  a.rows = static_cast<float*>(ws);
+  if (rows && (!ws || ws_bytes < row_bytes(g) + diff_bwd_part_bytes(g))) return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
+  a.rows = static_cast<uint8_t*>(ws);
+  a.splits = rows ? diff_bwd_splits(g) : 1;
+  a.part = a.splits > 1 ? reinterpret_cast<float*>(a.rows + row_bytes(g)) : nullptr;
   a.g.k_lens = k_lens;
   a.q1 = q1; a.q2 = q2; a.k1 = k1; a.k2 = k2; a.v = v; a.lam = lam; a.o = o; a.o2 = o2; a.lse = lse; a.dO = dO;
   a.dq1 = dq1; a.dq2 = dq2; a.dk1 = dk1; a.dk2 = dk2; a.dv = dv; a.dlam = dlam;

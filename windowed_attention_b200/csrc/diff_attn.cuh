@@ -244,18 +244,30 @@ struct DiffFwdArgs {
   int splits;
   int* err;
 };
-// Row constants of the backward, for every box of 64 query rows of every
-// (sequence, key head), [boxes][kRowArrays][64]: -log2e lse1, -log2e lse2,
-// -dO.O1, -dO.O2, -lambda, and what dlambda sums (-sum_k P2 dP, by the dq
-// kernel). Rows without a query: -inf, -inf and zeros, so that P = 0.
-enum { kRowL1 = 0, kRowL2, kRowD1, kRowD2, kRowLam, kRowSum, kRowArrays };
+// Row constants of the backward for every box of 64 query rows of every
+// (sequence, key head). First what the key-side kernel streams:
+//  * a [64][16] operand tile (32-byte rows, swizzled) whose columns hold
+//    c = -lse / scale of both maps and -D_1, each as three 16-bit terms that
+//    add up to 33 or 24 bits: 256 h + m + l. One more K step against a
+//    constant operand adds them to S_1, S_2 and dP inside the products.
+//  * D_1 - D_2 and -lambda of each row.
+// Then what the query-side kernel reads once: -log2e lse1, -log2e lse2, -D_1,
+// -D_2, and where it leaves -sum_k P_2 dP for dlambda. Rows without a query
+// hold zeros: their Q and dO are zeros, and so is what they add.
+struct DiffRows {
+  static constexpr int kTile = 64 * 16 * 2;
+  static constexpr int kDelta = kTile, kLam = kTile + 256, kStream = kTile + 512;   // bytes streamed
+  static constexpr int kL1 = kStream, kL2 = kL1 + 256, kD1 = kL2 + 256, kD2 = kD1 + 256, kSum = kD2 + 256, kBytes = kSum + 256;
+};
 struct DiffBwdArgs {
   DiffGeom g;
   const void *q1, *q2, *k1, *k2, *v, *lam, *o, *o2, *dO;
   const float* lse;
   void *dq1, *dq2, *dk1, *dk2, *dv, *dlam;
-  float* rows;
+  uint8_t* rows;     // [sequences * key heads][boxes] of DiffRows
   int boxes;         // of one (sequence, key head), an even number
+  float* part;       // key-side sums of `splits` shares of the rows, [unit][key tile][split][128][2 d + dv]; null without
+  int splits;
   int* err;
 };
 inline int diff_sequences(const DiffGeom& g) { return g.window ? g.batch * g.nwx * g.nwy : g.batch; }
@@ -268,6 +280,8 @@ inline int diff_max_k_boxes(const DiffGeom& g) { return ceil_div(diff_span_x(g, 
 inline int diff_class(int d, int dv) { return d <= 16 && dv <= 32 ? 0 : (d <= 32 && dv <= 64 ? 1 : 2); }
 int diff_splits(const DiffGeom& g);
 size_t diff_split_bytes(const DiffGeom& g);
+int diff_bwd_splits(const DiffGeom& g);
+size_t diff_bwd_part_bytes(const DiffGeom& g);
 // Tensor maps (columns, heads, x, y, batch) of the query and the key side with
 // their boxes; `cols` is the width of an operand atom.
 bool diff_map(CUtensorMap* map, const DiffGeom& g, bool query, bool f16, const void* p, const DiffStrides& s, int e, int cols);

@@ -13,9 +13,13 @@
 //  * dq: one CTA owns 128 query rows and streams key boxes of 64. It also sums
 //    P_2 dP in fp32, which spares dlambda the rounding of a stored O_2.
 //  * dkv: one CTA owns 128 keys of a key head and streams query boxes, keys in
-//    the TMEM lanes (S_i^T = K_i Q_i^T); the last CTAs add up dlambda. Every
-//    sum has one owner and a fixed order: the same bits on every run, no
-//    atomics.
+//    the TMEM lanes (S_i^T = K_i Q_i^T); the last CTAs add up dlambda. Per-row
+//    constants lie along its columns: reading them for every element took
+//    three quarters of the shared-memory pipe, so lse and D_1 enter inside the
+//    products, as one more K step. Where the key tiles alone leave SMs idle or
+//    a causal mask gives the first ones most of the work, each one's rows are
+//    split over CTAs, whose fp32 sums a fourth launch adds. Every sum has one
+//    owner and a fixed order: the same bits on every run, no atomics.
 // Both recompute S_i and dP: the alternative, one kernel that adds its dQ
 // tiles to memory, needs atomics, whose order changes the result.
 //
@@ -116,20 +120,39 @@ __global__ void __launch_bounds__(256) diff_attn_rows_kernel(const DiffBwdArgs a
     d2 += __shfl_xor_sync(0xFFFFFFFFu, d2, o);
   }
   if (lane != 0) return;
-  float l[2] = {-INFINITY, -INFINITY};   // minus the log-sum-exp: a row that saw nothing has P = 2^(S - inf) = 0
+  // a row that saw nothing (lse -inf) is masked wherever it is met: any finite value will do
+  float l[2] = {0.f, 0.f};
   if (live)
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
       const float v = a.lse[((static_cast<long long>(m) * g.batch + s.b) * g.q_heads + hq) * g.q_len + token];
-      l[m] = v == -INFINITY ? -INFINITY : fmaf(-kDiffLog2e, v, kShift<F16>);
+      if (v != -INFINITY) l[m] = fmaf(-kDiffLog2e, v, kShift<F16>);
     }
-  float* w = a.rows + box_at * (kRowArrays * 64) + r6;
-  w[kRowL1 * 64] = l[0];
-  w[kRowL2 * 64] = l[1];
-  w[kRowD1 * 64] = -d1;
-  w[kRowD2 * 64] = -d2;
-  w[kRowLam * 64] = live ? -lam : 0.f;
-  w[kRowSum * 64] = 0.f;
+  uint8_t* w = a.rows + box_at * DiffRows::kBytes;
+  const auto put = [&](int at, float v) { *reinterpret_cast<float*>(w + at + 4 * r6) = v; };
+  put(DiffRows::kDelta, d1 - d2);
+  put(DiffRows::kLam, live ? -lam : 0.f);
+  put(DiffRows::kL1, l[0]);
+  put(DiffRows::kL2, l[1]);
+  put(DiffRows::kD1, -d1);
+  put(DiffRows::kD2, -d2);
+  put(DiffRows::kSum, 0.f);
+  // x = 256 h + m + l in the operand type, each term the rounding of what is left
+  const auto terms = [](float x, float& h, float& m, float& r) {
+    h = diff_lo<F16>(diff_pack<F16>(x * (1.f / 256.f), 0.f));
+    const float y = fmaf(-256.f, h, x);
+    m = diff_lo<F16>(diff_pack<F16>(y, 0.f));
+    r = y - m;
+  };
+  const float inv = 1.f / g.scale_log2;
+  float t[9];
+  terms(l[0] * inv, t[0], t[1], t[2]);
+  terms(l[1] * inv, t[3], t[4], t[5]);
+  terms(-d1, t[6], t[7], t[8]);
+  using TT = DiffTile<64, 16>;
+  *reinterpret_cast<uint4*>(w + TT::offset(r6, 0)) = make_uint4(diff_pack<F16>(t[0], t[1]), diff_pack<F16>(t[2], t[3]), diff_pack<F16>(t[4], t[5]),
+                                                              diff_pack<F16>(t[6], t[7]));
+  *reinterpret_cast<uint4*>(w + TT::offset(r6, 1)) = make_uint4(diff_pack<F16>(t[8], 0.f), 0u, 0u, 0u);
 }
 
 // ------------------------------------------------------------------- dQ kernel
@@ -327,8 +350,9 @@ diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_cons
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t = tmem + lane_off + Lay::BUF * p + 32 * h;
     const DiffRow q = diff_query_row(g, s, 2 * qt + (row >> 6), row & 63);
-    float* c = a.rows + ((static_cast<long long>(unit) * a.boxes + 2 * qt + (row >> 6)) * kRowArrays) * 64 + (row & 63);
-    const float l1 = c[kRowL1 * 64], l2 = c[kRowL2 * 64], d1 = c[kRowD1 * 64], d2 = c[kRowD2 * 64], nlam = c[kRowLam * 64];
+    uint8_t* c = a.rows + (static_cast<long long>(unit) * a.boxes + 2 * qt + (row >> 6)) * DiffRows::kBytes + 4 * (row & 63);
+    const auto get = [&](int at) { return *reinterpret_cast<const float*>(c + at); };
+    const float l1 = get(DiffRows::kL1), l2 = get(DiffRows::kL2), d1 = get(DiffRows::kD1), d2 = get(DiffRows::kD2), nlam = get(DiffRows::kLam);
     const int seen = q.live ? diff_visible(g, s, q.x) : 0x7FFFFFFF;
     const bool warp_live = __any_sync(0xFFFFFFFFu, q.live);
     const uint64_t sl2 = f2_pack(g.scale_log2, g.scale_log2), L1 = f2_pack(l1, l1), L2 = f2_pack(l2, l2), D1 = f2_pack(d1, d1), D2 = f2_pack(d2, d2);
@@ -387,7 +411,7 @@ diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_cons
     tc_fence_after();
     if (ok && warp_live && *abort_flag == 0u) {
       if (w == 0 && q.live)
-        c[kRowSum * 64] = -kUnshift<F16> * ((sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]));
+        *reinterpret_cast<float*>(c + DiffRows::kSum) = -kUnshift<F16> * ((sums[row] + sums[128 + row]) + (sums[256 + row] + sums[384 + row]));
       // warpgroup (p, h) stores columns h D / 2 .. of dQ_(p + 1); without a key in sight the gradient is zero
       const float f = g.scale * kUnshift<F16>;
       uint16_t* out = static_cast<uint16_t*>(p ? a.dq2 : a.dq1);
@@ -427,10 +451,12 @@ struct DkvLay {
   static constexpr int NB = DV <= 64 ? 2 : 1;
   static constexpr int PER = 16 * NB;      // query rows of a warpgroup's share
   static constexpr int OWN = 2 * TK::BYTES + TV::BYTES;
-  static constexpr int CONSTS = kRowArrays * kStream * 4;
+  using TA = DiffTile<kOwn, 16>;           // the constant operands of the row constants' K step
+  static constexpr int CONSTS = DiffRows::kStream;
   static constexpr int STAGE = (2 * TQ::BYTES + TO::BYTES + CONSTS + 1023) / 1024 * 1024;
-  static constexpr int NS = DV <= 64 ? 4 : 3;
-  static constexpr int OFF_ST = OWN;
+  static constexpr int NS = DV <= 64 ? 4 : 2;
+  static constexpr int OFF_A = OWN;
+  static constexpr int OFF_ST = OFF_A + 3 * TA::BYTES;
   static constexpr int OFF_X = OFF_ST + NS * STAGE;
   static constexpr int X = 3 * TP::BYTES;
   static constexpr int OFF_BAR = OFF_X + NB * X;
@@ -460,11 +486,12 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
   const DiffGeom& g = a.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  int u = blockIdx.x / k_tiles;
+  // work unit: (sequence, key head), key tile, split of its rows
+  const int item = blockIdx.x / a.splits, sp = blockIdx.x - item * a.splits, u = item / k_tiles;
   if (u >= units) {
     // dlambda of one head: its rows' sums over every sequence, each thread a
     // strided share, then a tree
-    const int hq = blockIdx.x - units * k_tiles, hk = hq / g.group, gh = hq - hk * g.group;
+    const int hq = blockIdx.x - units * k_tiles * a.splits, hk = hq / g.group, gh = hq - hk * g.group;
     const int per = g.tcq * g.trq;
     const long long total = static_cast<long long>(units / g.kv_heads) * a.boxes * per;
     float sum = 0.f;
@@ -472,7 +499,8 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       const long long box = i / per;
       const int idx = static_cast<int>(i - box * per);
       const long long seq = box / a.boxes;
-      sum += a.rows[(((seq * g.kv_heads + hk) * a.boxes + (box - seq * a.boxes)) * kRowArrays + kRowSum) * 64 + idx * g.group + gh];
+      sum += *reinterpret_cast<const float*>(a.rows + ((seq * g.kv_heads + hk) * a.boxes + (box - seq * a.boxes)) * DiffRows::kBytes +
+                                             DiffRows::kSum + 4 * (idx * g.group + gh));
     }
     float* red = reinterpret_cast<float*>(smem);
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -497,7 +525,7 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
   uint64_t* done = s_full + 8;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(smem + Lay::OFF_MISC);
   volatile uint32_t* abort_flag = tmem_holder + 1;
-  const int kt = blockIdx.x - u * k_tiles;              // with a causal mask the first keys have the most rows
+  const int kt = item - u * k_tiles;                    // with a causal mask the first keys have the most rows
   const int unit = u, hk = u % g.kv_heads;
   const DiffSeq s = diff_sequence(g, u / g.kv_heads);
   const int all = g.window ? s.wk : g.k_len;            // keys whose gradients are written
@@ -511,7 +539,9 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     first = min(max(key0 - s.wk + s.wq, 0), s.wq);
     full = min(max(min(key0 + kOwn, s.wk) - 1 - s.wk + s.wq, 0), s.wq);
   }
-  const int j0 = first / g.tcq * (g.causal ? 1 : 0), n = !g.window && (key0 >= s.wk || first >= s.wq) ? 0 : q_boxes - j0;
+  const int j_all = g.causal ? first / g.tcq : 0, n_all = !g.window && (key0 >= s.wk || first >= s.wq) ? 0 : q_boxes - j_all;
+  const int from_box = static_cast<int>(wide(n_all, sp) / a.splits);
+  const int j0 = j_all + from_box, n = static_cast<int>(wide(n_all, sp + 1) / a.splits) - from_box;
   const int q_rows = g.tcq * g.trq * g.group;
   const bool clear = g.window && (s.wq % g.tcq || s.hq % g.trq);   // boxes with another window's rows
 
@@ -541,8 +571,19 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     // rows of a stage that no load writes are zeros
     for (int i = Lay::OFF_ST + threadIdx.x * 16; i < Lay::OFF_X; i += kThreads * 16)
       *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
-    fence_proxy_async_smem();
   }
+  // three [128][16] operands, every row alike: 256, 1, 1 in the columns of S_1's, S_2's and dP's terms
+  for (int i = threadIdx.x; i < 3 * kOwn * 2; i += kThreads) {
+    const int which = i / (kOwn * 2), r = i / 2 % kOwn, chunk = i & 1;
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const auto at = [&](int c) { return c == 3 * which ? 256.f : (c == 3 * which + 1 || c == 3 * which + 2 ? 1.f : 0.f); };
+      w[e] = diff_pack<F16>(at(8 * chunk + 2 * e), at(8 * chunk + 2 * e + 1));
+    }
+    *reinterpret_cast<uint4*>(smem + Lay::OFF_A + which * Lay::TA::BYTES + Lay::TA::offset(r, chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -563,7 +604,7 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         TV::load(smem + 2 * TK::BYTES, h, &tm_v, own, hk, x, y, s.b);
       }
       const uint32_t bytes = 2 * TQ::box_bytes(q_rows) + TO::box_bytes(q_rows) + Lay::CONSTS;
-      const float* consts = a.rows + (static_cast<long long>(unit) * a.boxes + j0) * (kRowArrays * 64);
+      const uint8_t* consts = a.rows + (static_cast<long long>(unit) * a.boxes + j0) * DiffRows::kBytes;
       int by = j0 / q_nx, bx = j0 - by * q_nx, issued = 0;
       uint64_t* to_full = clear ? raw : st_full;
       for (int i = 0; i < n; ++i) {
@@ -575,7 +616,7 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         TQ::load(to, 0, &tm_q1, &to_full[st], hk * g.group, x, y, s.b);
         TQ::load(to + TQ::BYTES, 0, &tm_q2, &to_full[st], hk * g.group, x, y, s.b);
         TO::load(to + 2 * TQ::BYTES, 0, &tm_do, &to_full[st], hk * g.group, x, y, s.b);
-        bulk_load(to + 2 * TQ::BYTES + TO::BYTES, consts + static_cast<long long>(i) * (kRowArrays * 64), Lay::CONSTS, &to_full[st]);
+        bulk_load(to + 2 * TQ::BYTES + TO::BYTES, consts + static_cast<long long>(i) * DiffRows::kBytes, Lay::CONSTS, &to_full[st]);
         issued = i + 1;
         if (++bx == q_nx) {
           bx = 0;
@@ -609,6 +650,8 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       const uint32_t id_s = diff_idesc(F16, kStream, false);
       const uint32_t id_k = diff_idesc(F16, (g.d + 15) / 16 * 16, true), id_v = diff_idesc(F16, (g.dv + 15) / 16 * 16, true);
       const uint64_t k1 = TK::kmajor(so), k2 = TK::kmajor(so + TK::BYTES), v = TV::kmajor(so + 2 * TK::BYTES), x = TP::kmajor(sx);
+      using TC = DiffTile<kStream, 16>;
+      const uint64_t ca = Lay::TA::kmajor(so + Lay::OFF_A), cb = TC::kmajor(sst + 2 * TQ::BYTES + TO::BYTES);
       const uint64_t qk = TQ::kmajor(sst), dk = TO::kmajor(sst + 2 * TQ::BYTES), qm = TQ::mnmajor(sst), dm = TO::mnmajor(sst + 2 * TQ::BYTES);
       bool ok = warp_wait(own, 0, wc, SITE_OWN);
       int st = 0;
@@ -623,8 +666,11 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
           if (ok && elect_one()) {
             tc_fence_after();
             diff_mma_kk<TK, TQ, D / 16>(t, k1, qk + at, id_s);
+            umma_ss(t, ca, cb + at, id_s, 1u);
             diff_mma_kk<TK, TQ, D / 16>(t + Lay::S2, k2, qk + at + (TQ::BYTES >> 4), id_s);
+            umma_ss(t + Lay::S2, ca + (Lay::TA::BYTES >> 4), cb + at, id_s, 1u);
             diff_mma_kk<TV, TO, DV / 16>(t + Lay::DP, v, dk + at, id_s);
+            umma_ss(t + Lay::DP, ca + 2 * (Lay::TA::BYTES >> 4), cb + at, id_s, 1u);
             umma_commit(&s_full[bb]);
             umma_commit(&st_empty[st]);
           }
@@ -662,6 +708,10 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     const uint32_t t = tmem + lane_off + Lay::BUF * p + Lay::PER * part;
     const uint64_t sl2 = f2_pack(g.scale_log2, g.scale_log2);
     const int key = key0 + row;   // of a causal sequence
+    // one query head a key head: its lambda in a register
+    const bool one_head = g.group_magic == 0u;
+    const float nl = one_head ? -diff_lambda<F16>(a.lam, g.lam_f32, hk) : 0.f;
+    const ulonglong2 nlam = {f2_pack(nl, nl), f2_pack(nl, nl)};
     bool ok = true;
     for (int j = p; j < n; j += NB) {
       const int st = j % NS, round = NB == 2 ? j >> 1 : j;
@@ -669,8 +719,8 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       ok = ok && warp_wait(&s_full[p], round & 1, wc, SITE_S_FULL);
       if (!ok) break;
       tc_fence_after();
-      const float* cs =
-          reinterpret_cast<const float*>(smem + Lay::OFF_ST + st * Lay::STAGE + 2 * TQ::BYTES + TO::BYTES) + Lay::PER * part;
+      const float* cs = reinterpret_cast<const float*>(smem + Lay::OFF_ST + st * Lay::STAGE + 2 * TQ::BYTES + TO::BYTES + DiffRows::kDelta) +
+                        Lay::PER * part;   // D_1 - D_2; -lambda 64 further
       const int x0 = (j0 + j) * g.tcq;                 // first query of the box
       const bool edge = g.causal && x0 < full;
 #pragma unroll
@@ -702,19 +752,19 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
           for (int e = 0; e < 2; ++e) {   // four rows' constants a load
             const int i = 8 * q + 4 * e;
             const ulonglong2* quad = reinterpret_cast<const ulonglong2*>(cs + 16 * cc + i);
-            const ulonglong2 L1 = quad[kRowL1 * 16], L2 = quad[kRowL2 * 16], D1 = quad[kRowD1 * 16], D2 = quad[kRowD2 * 16],
-                             NL = quad[kRowLam * 16];
+            const ulonglong2 DD = quad[0];
+            const ulonglong2 NL = one_head ? nlam : quad[16];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
               const int at = i + 2 * f;
-              const uint64_t dd = raw_pair(dp + at);
-              const uint64_t y1 = f2_fma(raw_pair(s1 + at), sl2, f ? L1.y : L1.x), y2 = f2_fma(raw_pair(s2 + at), sl2, f ? L2.y : L2.x);
+              const uint64_t t1 = raw_pair(dp + at);
               const bool poly = 2 * e + f + 4 * q < POLY;
+              const uint64_t y1 = f2_mul(raw_pair(s1 + at), sl2), y2 = f2_mul(raw_pair(s2 + at), sl2);
               const uint64_t p1 = poly ? exp2_pair<true>(y1) : exp2_pair<false>(y1);
               const uint64_t p2 = f2_mul(poly ? exp2_pair<true>(y2) : exp2_pair<false>(y2), f ? NL.y : NL.x);
               pp[2 * e + f] = pack_pair<F16>(f2_add(p1, p2));
-              x1[2 * e + f] = pack_pair<F16>(f2_mul(p1, f2_add(dd, f ? D1.y : D1.x)));
-              x2[2 * e + f] = pack_pair<F16>(f2_mul(p2, f2_add(dd, f ? D2.y : D2.x)));
+              x1[2 * e + f] = pack_pair<F16>(f2_mul(p1, t1));
+              x2[2 * e + f] = pack_pair<F16>(f2_mul(p2, f2_add(t1, f ? DD.y : DD.x)));
             }
           }
           if (cc == 0 && q == 0 && round >= 1) {
@@ -743,23 +793,32 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       const int x = (box - by * k_nx) * g.tck + (c & (g.tck - 1)), y = by * g.trk + (c >> g.lk);
       const bool live = x < all && y < s.hk, real = n > 0 && x < s.wk;   // keys behind the length have gradient zero
       const int token = live ? s.token(x, y) : 0;
-      // warpgroup w stores its quarter of the columns of each gradient
-      auto store = [&](uint32_t col, int cols, uint16_t* out, int width, float f) {
+      // warpgroup w stores its quarter of the columns of each gradient: results, or this split's sums
+      const int width_all = 2 * g.d + g.dv;
+      float* part = a.part ? a.part + (static_cast<long long>(blockIdx.x) * kOwn + row) * width_all : nullptr;
+      auto store = [&](uint32_t col, int cols, uint16_t* out, int width, float f, int at) {
         const int share = cols >= 32 ? cols / 4 : 8;
         for (int c0 = w * share; c0 < min(cols, (w + 1) * share); c0 += 8) {
           uint32_t v[8], o[4];
           tmem_ld8(tmem + lane_off + col + c0, v);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            o[e] = real ? diff_pack<F16>(__uint_as_float(v[2 * e]) * f, __uint_as_float(v[2 * e + 1]) * f) : 0u;
-          if (live && c0 < width) *reinterpret_cast<uint4*>(out + c0) = make_uint4(o[0], o[1], o[2], o[3]);
+          for (int e = 0; e < 8; ++e) v[e] = real ? __float_as_uint(__uint_as_float(v[e]) * f) : 0u;
+          if (c0 >= width) continue;
+          if (part) {
+            *reinterpret_cast<uint4*>(part + at + c0) = make_uint4(v[0], v[1], v[2], v[3]);
+            *reinterpret_cast<uint4*>(part + at + c0 + 4) = make_uint4(v[4], v[5], v[6], v[7]);
+            continue;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[e] = diff_pack<F16>(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+          if (live) *reinterpret_cast<uint4*>(out + c0) = make_uint4(o[0], o[1], o[2], o[3]);
         }
       };
       const long long kv = s.b * g.v.b + wide(token, g.v.t) + wide(hk, g.v.h), kk = s.b * g.k.b + wide(token, g.k.t) + wide(hk, g.k.h);
-      store(Lay::V, DV, static_cast<uint16_t*>(a.dv) + kv, g.dv, kUnshift<F16>);
-      store(Lay::K1, D, static_cast<uint16_t*>(a.dk1) + kk, g.d, g.scale * kUnshift<F16>);
-      store(Lay::K2, D, static_cast<uint16_t*>(a.dk2) + kk, g.d, g.scale * kUnshift<F16>);
+      store(Lay::V, DV, static_cast<uint16_t*>(a.dv) + kv, g.dv, kUnshift<F16>, 2 * g.d);
+      store(Lay::K1, D, static_cast<uint16_t*>(a.dk1) + kk, g.d, g.scale * kUnshift<F16>, 0);
+      store(Lay::K2, D, static_cast<uint16_t*>(a.dk2) + kk, g.d, g.scale * kUnshift<F16>, g.d);
     }
   }
   tc_fence_before();
@@ -770,13 +829,45 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
   }
 }
 
+// The splits' sums of one key row, in their order; a thread owns eight columns.
+template <bool F16>
+__global__ void __launch_bounds__(256) diff_attn_dkv_join_kernel(const DiffBwdArgs a, int k_tiles, long long threads) {
+  const DiffGeom& g = a.g;
+  const long long at = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (at >= threads) return;
+  const int width = 2 * g.d + g.dv, pieces = width / 8;
+  const long long row_at = at / pieces;
+  const int c = static_cast<int>(at - row_at * pieces) * 8, row = static_cast<int>(row_at % kOwn);
+  const long long tile = row_at / kOwn;
+  const int unit = static_cast<int>(tile / k_tiles), kt = static_cast<int>(tile - static_cast<long long>(unit) * k_tiles), hk = unit % g.kv_heads;
+  const DiffSeq s = diff_sequence(g, unit / g.kv_heads);
+  const int all = g.window ? s.wk : g.k_len, k_nx = ceil_div(all, g.tck);
+  const int box = 2 * kt + (row >> 6), cc = row & 63, by = box / k_nx;
+  const int x = (box - by * k_nx) * g.tck + (cc & (g.tck - 1)), y = by * g.trk + (cc >> g.lk);
+  if (x >= all || y >= s.hk) return;
+  float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  const float* p = a.part + (tile * a.splits * kOwn + row) * width + c;
+  for (int i = 0; i < a.splits; ++i, p += static_cast<long long>(kOwn) * width) {
+    const float4 lo = reinterpret_cast<const float4*>(p)[0], hi = reinterpret_cast<const float4*>(p)[1];
+    v[0] += lo.x; v[1] += lo.y; v[2] += lo.z; v[3] += lo.w;
+    v[4] += hi.x; v[5] += hi.y; v[6] += hi.z; v[7] += hi.w;
+  }
+  const int token = s.token(x, y);
+  const long long kk = s.b * g.k.b + wide(token, g.k.t) + wide(hk, g.k.h);
+  uint16_t* out = c < g.d       ? static_cast<uint16_t*>(a.dk1) + kk + c
+                  : c < 2 * g.d ? static_cast<uint16_t*>(a.dk2) + kk + c - g.d
+                                : static_cast<uint16_t*>(a.dv) + s.b * g.v.b + wide(token, g.v.t) + wide(hk, g.v.h) + c - 2 * g.d;
+  *reinterpret_cast<uint4*>(out) =
+      make_uint4(diff_pack<F16>(v[0], v[1]), diff_pack<F16>(v[2], v[3]), diff_pack<F16>(v[4], v[5]), diff_pack<F16>(v[6], v[7]));
+}
+
 template <int D, int DV, bool F16>
 cudaError_t launch_class(const DiffBwdArgs& a, cudaStream_t stream) {
   const DiffGeom& g = a.g;
   const long long units = static_cast<long long>(diff_sequences(g)) * g.kv_heads;
   const int q_tiles = a.boxes / 2, k_tiles = ceil_div(diff_max_k_boxes(g), 2);
   constexpr int LPR = DV / 8;
-  const long long row_ctas = units * a.boxes * LPR / 4, q_ctas = units * q_tiles, k_ctas = units * k_tiles + g.q_heads;
+  const long long row_ctas = units * a.boxes * LPR / 4, q_ctas = units * q_tiles, k_ctas = units * k_tiles * a.splits + g.q_heads;
   if (row_ctas > 0x7FFFFFFFll || q_ctas > 0x7FFFFFFFll || k_ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
   using TK = DiffTile<kOwn, D>;
   using TV = DiffTile<kOwn, DV>;
@@ -799,10 +890,32 @@ cudaError_t launch_class(const DiffBwdArgs& a, cudaStream_t stream) {
   // k_tiles 0: dlambda alone, with no tiles before it
   dkv<<<static_cast<unsigned>(k_ctas), kThreads, DkvLay<D, DV>::ALLOC, stream>>>(q1, q2, dO, k1, k2, v, a, k_tiles > 0 ? k_tiles : 1,
                                                                                k_tiles > 0 ? static_cast<int>(units) : 0);
+  if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
+  const long long threads = units * k_tiles * kOwn * ((2 * g.d + g.dv) / 8);
+  if (threads <= 0) return cudaSuccess;
+  diff_attn_dkv_join_kernel<F16><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a, k_tiles, threads);
   return cudaGetLastError();
 }
 
 }  // namespace
+
+// Shares of a key tile's rows: one where there are three key tiles an SM;
+// else so many that the longest share is two thirds of an SM's part of all the
+// work, of eight boxes at least.
+int diff_bwd_splits(const DiffGeom& g) {
+  const long long k_tiles = ceil_div(diff_max_k_boxes(g), 2), boxes = diff_max_q_boxes(g);
+  const long long tiles = static_cast<long long>(diff_sequences(g)) * g.kv_heads * k_tiles;
+  if (tiles == 0 || boxes < 16 || tiles >= 3ll * sm_count()) return 1;
+  const long long total = tiles * boxes / (g.causal ? 2 : 1);   // boxes of all tiles
+  const long long want = (3 * boxes * sm_count() + 2 * total - 1) / (2 * total), most = boxes / 8;
+  const long long s = want < most ? want : most;
+  return static_cast<int>(s < 1 ? 1 : (s < 16 ? s : 16));
+}
+
+size_t diff_bwd_part_bytes(const DiffGeom& g) {
+  const int s = diff_bwd_splits(g);
+  return s > 1 ? static_cast<size_t>(diff_sequences(g)) * g.kv_heads * ceil_div(diff_max_k_boxes(g), 2) * s * kOwn * (2 * g.d + g.dv) * sizeof(float) : 0;
+}
 
 cudaError_t launch_diff_attn_bwd(const DiffBwdArgs& a, bool f16, cudaStream_t stream) {
   switch (diff_class(a.g.d, a.g.dv)) {
