@@ -38,12 +38,6 @@
 namespace rib {
 namespace {
 
-#ifndef RIB_DIFF_POLY_Q
-#define RIB_DIFF_POLY_Q 0
-#endif
-#ifndef RIB_DIFF_POLY_K
-#define RIB_DIFF_POLY_K 0
-#endif
 constexpr int kOwn = 128, kStream = 64;
 constexpr int kWarpS = 16, kWarpX = 17, kWarpLoad = 18, kWarpClear = 19;
 constexpr int kThreads = 32 * 20;
@@ -62,17 +56,12 @@ constexpr float kShift = F16 ? 6.f : 0.f;
 template <bool F16>
 constexpr float kUnshift = F16 ? 1.f / 64.f : 1.f;
 
-template <bool POLY>
+// All by the MUFU: the polynomial of the forward made both kernels slower (2 of
+// 8 pairs: 2.22 -> 2.25 ms for a 2x96x96 training call).
 __device__ __forceinline__ uint64_t exp2_pair(uint64_t x) {
-  float x0, x1, y0, y1;
+  float x0, x1;
   f2_unpack(x, x0, x1);
-  if constexpr (POLY) {
-    diff_exp2_poly(x0, x1, y0, y1);
-  } else {
-    y0 = ex2_approx(x0);
-    y1 = ex2_approx(x1);
-  }
-  return f2_pack(y0, y1);
+  return f2_pack(ex2_approx(x0), ex2_approx(x1));
 }
 template <bool F16>
 __device__ __forceinline__ uint32_t pack_pair(uint64_t x) {
@@ -171,12 +160,14 @@ struct DqLay {
   static constexpr int NBAR = 1 + 3 * NS + 6 + 1;      // own, st_full, st_empty, raw, s_full[2], x_full[2], x_done[2], done
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
-  // two buffers of S_1, S_2, dP (64 columns each); dS_i overwrites the first
-  // half of each 32 columns of S_i
+  // Two buffers of S_1, S_2, dP (64 columns each); dS_i overwrites the first
+  // half of each 32 columns of S_i. Columns of its own for dS, with S freed as
+  // soon as it was in registers, cost more in barriers than they saved (0.87
+  // for 0.77 ms at 2x96x96).
   static constexpr uint32_t BUF = 192, Q1 = 384, Q2 = 448, COLS = 512;
 };
 
-template <int D, int DV, bool F16, int POLY>
+template <int D, int DV, bool F16>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
                     const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k1,
@@ -386,9 +377,7 @@ diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_cons
           for (int i = 0; i < 8; ++i) {
             const uint64_t dd = raw_pair(dp + 2 * i);
             const uint64_t y1 = f2_fma(raw_pair(s1 + 2 * i), sl2, L1), y2 = f2_fma(raw_pair(s2 + 2 * i), sl2, L2);
-            const bool poly = i < POLY;
-            const uint64_t p1 = poly ? exp2_pair<true>(y1) : exp2_pair<false>(y1);
-            const uint64_t p2 = poly ? exp2_pair<true>(y2) : exp2_pair<false>(y2);
+            const uint64_t p1 = exp2_pair(y1), p2 = exp2_pair(y2);
             sum = f2_fma(p2, dd, sum);
             x1[i] = pack_pair<F16>(f2_mul(p1, f2_add(dd, D1)));
             x2[i] = pack_pair<F16>(f2_mul(f2_mul(p2, NL), f2_add(dd, D2)));
@@ -454,9 +443,11 @@ struct DkvLay {
   using TA = DiffTile<kOwn, 16>;           // the constant operands of the row constants' K step
   static constexpr int CONSTS = DiffRows::kStream;
   static constexpr int STAGE = (2 * TQ::BYTES + TO::BYTES + CONSTS + 1023) / 1024 * 1024;
-  static constexpr int NS = DV <= 64 ? 4 : 2;
+  static constexpr int NS = DV <= 64 ? 4 : 3;
+  // the constant operands: shared memory, or (dv = 128) 24 spare columns of TMEM
+  static constexpr bool A_TMEM = DV > 64;
   static constexpr int OFF_A = OWN;
-  static constexpr int OFF_ST = OFF_A + 3 * TA::BYTES;
+  static constexpr int OFF_ST = OFF_A + (A_TMEM ? 0 : 3 * TA::BYTES);
   static constexpr int OFF_X = OFF_ST + NS * STAGE;
   static constexpr int X = 3 * TP::BYTES;
   static constexpr int OFF_BAR = OFF_X + NB * X;
@@ -464,11 +455,12 @@ struct DkvLay {
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
   static_assert(ALLOC <= 232448, "shared memory of an SM");
-  static constexpr uint32_t BUF = 192, S2 = 64, DP = 128, V = BUF * NB, K1 = V + DV, K2 = K1 + D, COLS = 512;
-  static_assert(K2 + D <= 512, "TMEM columns");
+  static constexpr uint32_t BUF = 192, S2 = 64, DP = 128, V = BUF * NB, K1 = V + DV, K2 = K1 + D, A = K2 + D, COLS = 512;
+  static_assert(A + (A_TMEM ? 24 : 0) <= 512, "TMEM columns");
 };
 
-template <int D, int DV, bool F16, int POLY>
+// ONE: a key head of one query head, whose lambda is a constant.
+template <int D, int DV, bool F16, bool ONE>
 __global__ void __launch_bounds__(kThreads, 1)
 diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
                      const __grid_constant__ CUtensorMap tm_do, const __grid_constant__ CUtensorMap tm_k1,
@@ -573,21 +565,35 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
   }
   // three [128][16] operands, every row alike: 256, 1, 1 in the columns of S_1's, S_2's and dP's terms
-  for (int i = threadIdx.x; i < 3 * kOwn * 2; i += kThreads) {
-    const int which = i / (kOwn * 2), r = i / 2 % kOwn, chunk = i & 1;
-    uint32_t w[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const auto at = [&](int c) { return c == 3 * which ? 256.f : (c == 3 * which + 1 || c == 3 * which + 2 ? 1.f : 0.f); };
-      w[e] = diff_pack<F16>(at(8 * chunk + 2 * e), at(8 * chunk + 2 * e + 1));
+  const auto constant = [](int which, int c) {
+    const auto at = [&](int i) { return i == 3 * which ? 256.f : (i == 3 * which + 1 || i == 3 * which + 2 ? 1.f : 0.f); };
+    return diff_pack<F16>(at(c), at(c + 1));
+  };
+  if (!Lay::A_TMEM)
+    for (int i = threadIdx.x; i < 3 * kOwn * 2; i += kThreads) {
+      const int which = i / (kOwn * 2), r = i / 2 % kOwn, c = 8 * (i & 1);
+      *reinterpret_cast<uint4*>(smem + Lay::OFF_A + which * Lay::TA::BYTES + Lay::TA::offset(r, i & 1)) =
+          make_uint4(constant(which, c), constant(which, c + 2), constant(which, c + 4), constant(which, c + 6));
     }
-    *reinterpret_cast<uint4*>(smem + Lay::OFF_A + which * Lay::TA::BYTES + Lay::TA::offset(r, chunk)) = make_uint4(w[0], w[1], w[2], w[3]);
-  }
   fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_holder;
+  if (Lay::A_TMEM) {
+    if (warp < 4) {
+      for (int which = 0; which < 3; ++which) {
+        uint32_t w[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = constant(which, 2 * e);
+        tmem_st8(tmem + (static_cast<uint32_t>(warp * 32) << 16) + Lay::A + 8 * which, w);
+      }
+      tmem_wait_st();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+  }
   const WaitCtx wc{abort_flag, a.err};
   const WaitCtx drain{tmem_holder + 2, a.err};
   const uint32_t so = smem_u32(smem), sst = so + Lay::OFF_ST, sx = so + Lay::OFF_X;
@@ -652,6 +658,10 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       const uint64_t k1 = TK::kmajor(so), k2 = TK::kmajor(so + TK::BYTES), v = TV::kmajor(so + 2 * TK::BYTES), x = TP::kmajor(sx);
       using TC = DiffTile<kStream, 16>;
       const uint64_t ca = Lay::TA::kmajor(so + Lay::OFF_A), cb = TC::kmajor(sst + 2 * TQ::BYTES + TO::BYTES);
+      const auto add_constants = [&](uint32_t d, int which, uint64_t b) {
+        if constexpr (Lay::A_TMEM) umma_ts(d, tmem + Lay::A + 8 * which, b, id_s, 1u);
+        else umma_ss(d, ca + static_cast<uint32_t>(which) * (Lay::TA::BYTES >> 4), b, id_s, 1u);
+      };
       const uint64_t qk = TQ::kmajor(sst), dk = TO::kmajor(sst + 2 * TQ::BYTES), qm = TQ::mnmajor(sst), dm = TO::mnmajor(sst + 2 * TQ::BYTES);
       bool ok = warp_wait(own, 0, wc, SITE_OWN);
       int st = 0;
@@ -666,11 +676,11 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
           if (ok && elect_one()) {
             tc_fence_after();
             diff_mma_kk<TK, TQ, D / 16>(t, k1, qk + at, id_s);
-            umma_ss(t, ca, cb + at, id_s, 1u);
+            add_constants(t, 0, cb + at);
             diff_mma_kk<TK, TQ, D / 16>(t + Lay::S2, k2, qk + at + (TQ::BYTES >> 4), id_s);
-            umma_ss(t + Lay::S2, ca + (Lay::TA::BYTES >> 4), cb + at, id_s, 1u);
+            add_constants(t + Lay::S2, 1, cb + at);
             diff_mma_kk<TV, TO, DV / 16>(t + Lay::DP, v, dk + at, id_s);
-            umma_ss(t + Lay::DP, ca + 2 * (Lay::TA::BYTES >> 4), cb + at, id_s, 1u);
+            add_constants(t + Lay::DP, 2, cb + at);
             umma_commit(&s_full[bb]);
             umma_commit(&st_empty[st]);
           }
@@ -708,9 +718,7 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     const uint32_t t = tmem + lane_off + Lay::BUF * p + Lay::PER * part;
     const uint64_t sl2 = f2_pack(g.scale_log2, g.scale_log2);
     const int key = key0 + row;   // of a causal sequence
-    // one query head a key head: its lambda in a register
-    const bool one_head = g.group_magic == 0u;
-    const float nl = one_head ? -diff_lambda<F16>(a.lam, g.lam_f32, hk) : 0.f;
+    const float nl = ONE ? -diff_lambda<F16>(a.lam, g.lam_f32, hk) : 0.f;
     const ulonglong2 nlam = {f2_pack(nl, nl), f2_pack(nl, nl)};
     bool ok = true;
     for (int j = p; j < n; j += NB) {
@@ -753,15 +761,13 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
             const int i = 8 * q + 4 * e;
             const ulonglong2* quad = reinterpret_cast<const ulonglong2*>(cs + 16 * cc + i);
             const ulonglong2 DD = quad[0];
-            const ulonglong2 NL = one_head ? nlam : quad[16];
+            const ulonglong2 NL = ONE ? nlam : quad[16];
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
               const int at = i + 2 * f;
               const uint64_t t1 = raw_pair(dp + at);
-              const bool poly = 2 * e + f + 4 * q < POLY;
               const uint64_t y1 = f2_mul(raw_pair(s1 + at), sl2), y2 = f2_mul(raw_pair(s2 + at), sl2);
-              const uint64_t p1 = poly ? exp2_pair<true>(y1) : exp2_pair<false>(y1);
-              const uint64_t p2 = f2_mul(poly ? exp2_pair<true>(y2) : exp2_pair<false>(y2), f ? NL.y : NL.x);
+              const uint64_t p1 = exp2_pair(y1), p2 = f2_mul(exp2_pair(y2), f ? NL.y : NL.x);
               pp[2 * e + f] = pack_pair<F16>(f2_add(p1, p2));
               x1[2 * e + f] = pack_pair<F16>(f2_mul(p1, t1));
               x2[2 * e + f] = pack_pair<F16>(f2_mul(p2, f2_add(t1, f ? DD.y : DD.x)));
@@ -876,8 +882,8 @@ cudaError_t launch_class(const DiffBwdArgs& a, cudaStream_t stream) {
       !diff_map(&dO, g, true, F16, a.dO, g.o, g.dv, TV::COLS) || !diff_map(&k1, g, false, F16, a.k1, g.k, g.d, TK::COLS) ||
       !diff_map(&k2, g, false, F16, a.k2, g.k, g.d, TK::COLS) || !diff_map(&v, g, false, F16, a.v, g.v, g.dv, TV::COLS))
     return cudaErrorInvalidValue;
-  auto dq = diff_attn_dq_kernel<D, DV, F16, RIB_DIFF_POLY_Q>;
-  auto dkv = diff_attn_dkv_kernel<D, DV, F16, RIB_DIFF_POLY_K>;
+  auto dq = diff_attn_dq_kernel<D, DV, F16>;
+  auto dkv = g.group == 1 ? diff_attn_dkv_kernel<D, DV, F16, true> : diff_attn_dkv_kernel<D, DV, F16, false>;
   cudaError_t e = cudaFuncSetAttribute(dq, cudaFuncAttributeMaxDynamicSharedMemorySize, DqLay<D, DV>::ALLOC);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(dkv, cudaFuncAttributeMaxDynamicSharedMemorySize, DkvLay<D, DV>::ALLOC);
   if (e != cudaSuccess) return e;

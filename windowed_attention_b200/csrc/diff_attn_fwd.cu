@@ -21,7 +21,9 @@
 //   then one warp        issues P V (its own stream: neither waits for the other)
 //   then one warp        TMA producer
 //   then one warp        clears the rows of a key box that are not the sequence's
-// TMEM: S of map m and parity q at 64 (2 q + m), O from column 256.
+// TMEM: S of map m and parity q at 64 (2 q + m), O from column 256. (P in columns
+// of its own, with S freed as soon as it was in registers, cost more in barriers
+// than it saved: 0.97 for 0.87 ms.)
 //
 // Bound: the exponentials, 2 per (query, key) pair: a tile of 128 x 64 x 2
 // takes 1024 cycles of the SM's MUFU, of which the FMA pipe takes over POLY of
@@ -33,9 +35,6 @@
 namespace rib {
 namespace {
 
-#ifndef RIB_DIFF_POLY_F
-#define RIB_DIFF_POLY_F 2
-#endif
 constexpr int kBK = 64;
 
 enum Site : int {
@@ -505,7 +504,9 @@ __global__ void __launch_bounds__(256) diff_attn_join_kernel(const DiffFwdArgs a
 template <int D, int DV, bool F16>
 cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
   using Lay = FwdLay<D, DV>;
-  constexpr int POLY = RIB_DIFF_POLY_F;
+  // Of 8 pairs, those on the FMA pipe: at dv <= 32 the softmax warps' own instructions bound too (window 64 map: 868 us
+  // with none, 872 with two); at 64 and 128 two are best (128 -> 124 us, 140 -> 134 us)
+  constexpr int POLY = DV <= 32 ? 0 : 2;
   auto kernel = diff_attn_fwd_kernel<D, DV, F16, POLY>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC);
   if (e != cudaSuccess) return e;
