@@ -173,6 +173,10 @@ rib_status rib_diff_attention(const rib_diff_attn_desc* d, const void* q1, const
   if (a.splits > 1) {
     if (!ws || ws_bytes < diff_split_bytes(a.g)) return bad(who, RIB_ERR_INVALID_ARG, "workspace missing or too small");
     a.part = static_cast<float*>(ws);
+    if (diff_few_rows(a.g)) {
+      a.quad = 1;
+      a.g.tcq = 32 / a.g.group;   // the rows of one lane quarter
+    }
   }
   a.g.k_lens = k_lens;
   a.q1 = q1; a.q2 = q2; a.k1 = k1; a.k2 = k2; a.v = v; a.lam = lam;

@@ -51,6 +51,8 @@ __device__ __forceinline__ int div_by(int t, uint32_t magic) {
 __host__ __device__ inline int ceil_div(int a, int b) { return (a + b - 1) / b; }
 __device__ __forceinline__ long long wide(int a, int b) { return static_cast<long long>(a) * b; }
 
+__device__ __forceinline__ int diff_row_token(const DiffGeom& g, int r) { return g.group_magic ? div_by(r, g.group_magic) : r; }
+
 // One sequence: a rectangle of queries wq x hq and one of keys wk x hk at (x0, y0) of batch item b.
 struct DiffSeq {
   int b, x0, y0, wq, hq, wk, hk, width;
@@ -163,11 +165,11 @@ struct DiffTile {
   __device__ static constexpr uint32_t kstep(int ks) { return (ks / (COLS / 16) * ATOM + ks % (COLS / 16) * 32) >> 4; }
   __device__ static __forceinline__ uint64_t mnmajor(uint32_t base) { return make_sdesc(base, ATOM, 8 * RB, SW); }
   __device__ static constexpr uint32_t mnstep(int ks) { return (ks * 16 * RB) >> 4; }
-  // One box into rows 64 half .. of the tile; columns behind the tensor's width
+  // One box into rows `row` .. of the tile; columns behind the tensor's width
   // arrive as zeros.
-  __device__ static __forceinline__ void load(uint8_t* tile, int half, const CUtensorMap* map, uint64_t* bar, int head, int x, int y, int b) {
+  __device__ static __forceinline__ void load(uint8_t* tile, int row, const CUtensorMap* map, uint64_t* bar, int head, int x, int y, int b) {
 #pragma unroll
-    for (int a = 0; a < D / COLS; ++a) tma_load_5d(tile + a * ATOM + half * 64 * RB, map, bar, a * COLS, head, x, y, b);
+    for (int a = 0; a < D / COLS; ++a) tma_load_5d(tile + a * ATOM + row * RB, map, bar, a * COLS, head, x, y, b);
   }
   __device__ static __forceinline__ uint32_t box_bytes(int rows) { return static_cast<uint32_t>(rows * D * 2); }
   // Zeros into a row, by `lanes` threads.
@@ -241,7 +243,7 @@ struct DiffFwdArgs {
   void *o, *o2;
   float* lse;        // [2][batch][q_heads][q_len] or null
   float* part;       // split keys: [splits][rows][2][dv] then [splits][rows][2] (log2 of the row sums); null without
-  int splits;
+  int splits, quad;  // CTAs of a query tile; the form for few rows
   int* err;
 };
 // Row constants of the backward for every box of 64 query rows of every
@@ -278,6 +280,8 @@ inline int diff_max_q_boxes(const DiffGeom& g) { return ceil_div(diff_span_x(g, 
 inline int diff_max_k_boxes(const DiffGeom& g) { return ceil_div(diff_span_x(g, g.k_len), g.tck) * ceil_div(diff_span_y(g), g.trk); }
 // The operand widths of the kernels: the smallest pair that holds d and dv.
 inline int diff_class(int d, int dv) { return d <= 16 && dv <= 32 ? 0 : (d <= 32 && dv <= 64 ? 1 : 2); }
+// Few query rows over split keys take a form of the kernel that splits them over its warps too.
+inline bool diff_few_rows(const DiffGeom& g) { return !g.window && static_cast<long long>(g.q_len) * g.group <= 32; }
 int diff_splits(const DiffGeom& g);
 size_t diff_split_bytes(const DiffGeom& g);
 int diff_bwd_splits(const DiffGeom& g);

@@ -241,9 +241,9 @@ diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_cons
       mbar_arrive_expect_tx(own, halves * (2 * TQ::box_bytes(q_rows) + TO::box_bytes(q_rows)));
       for (int h = 0; h < halves; ++h) {
         const int box = 2 * qt + h, by = box / nx_q, x = s.x0 + (box - by * nx_q) * g.tcq, y = s.y0 + by * g.trq;
-        TQ::load(smem, h, &tm_q1, own, hk * g.group, x, y, s.b);
-        TQ::load(smem + TQ::BYTES, h, &tm_q2, own, hk * g.group, x, y, s.b);
-        TO::load(smem + 2 * TQ::BYTES, h, &tm_do, own, hk * g.group, x, y, s.b);
+        TQ::load(smem, 64 * h, &tm_q1, own, hk * g.group, x, y, s.b);
+        TQ::load(smem + TQ::BYTES, 64 * h, &tm_q2, own, hk * g.group, x, y, s.b);
+        TO::load(smem + 2 * TQ::BYTES, 64 * h, &tm_do, own, hk * g.group, x, y, s.b);
       }
       const uint32_t bytes = 2 * TK::box_bytes(kStream) + TV::box_bytes(kStream);
       int bx = 0, by = 0, issued = 0;
@@ -605,9 +605,9 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       mbar_arrive_expect_tx(own, halves * (2 * TK::box_bytes(64) + TV::box_bytes(64)));
       for (int h = 0; h < halves; ++h) {
         const int box = 2 * kt + h, by = box / k_nx, x = s.x0 + (box - by * k_nx) * g.tck, y = s.y0 + by * g.trk;
-        TK::load(smem, h, &tm_k1, own, hk, x, y, s.b);
-        TK::load(smem + TK::BYTES, h, &tm_k2, own, hk, x, y, s.b);
-        TV::load(smem + 2 * TK::BYTES, h, &tm_v, own, hk, x, y, s.b);
+        TK::load(smem, 64 * h, &tm_k1, own, hk, x, y, s.b);
+        TK::load(smem + TK::BYTES, 64 * h, &tm_k2, own, hk, x, y, s.b);
+        TV::load(smem + 2 * TK::BYTES, 64 * h, &tm_v, own, hk, x, y, s.b);
       }
       const uint32_t bytes = 2 * TQ::box_bytes(q_rows) + TO::box_bytes(q_rows) + Lay::CONSTS;
       const uint8_t* consts = a.rows + (static_cast<long long>(unit) * a.boxes + j0) * DiffRows::kBytes;

@@ -57,6 +57,7 @@ struct FwdLay {
   static constexpr int NBAR = 1 + 3 * NS + 12 + 1;          // q, kv_full, kv_empty, raw, s[4], p[4], pv[4], done
   static constexpr int OFF_MISC = OFF_BAR + NBAR * 8;
   static constexpr int ALLOC = OFF_MISC + 16 + 1024;
+  static_assert((128 * 2 * DV + 256) * 4 <= OFF_L, "the quarters' outputs over the tiles");
   static constexpr uint32_t O = 256, COLS = 512;
 };
 
@@ -71,7 +72,11 @@ __device__ __forceinline__ float max_nan(float a, float b) {
   return d;
 }
 
-template <int D, int DV, bool F16, int POLY>
+// QUAD: one tile of at most 32 query rows over split keys (single tokens). The
+// rows stand in all four lane quarters; the warps of a quarter take 16 of a
+// box's 64 keys and leave zeros in P for the others; the four O of a row are
+// joined at the end. A fourth of the exponentials a warp, where they bound.
+template <int D, int DV, bool F16, int POLY, bool QUAD>
 __global__ void __launch_bounds__(FwdLay<D, DV>::kThreads, 1)
 diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_constant__ CUtensorMap tm_q2,
                      const __grid_constant__ CUtensorMap tm_k1, const __grid_constant__ CUtensorMap tm_k2,
@@ -152,12 +157,12 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
   if (warp == kWarpLoad) {
     // --------------------------------------------------------- TMA producer
     if (lane == 0 && n > 0) {
-      const int nx_q = ceil_div(s.wq, g.tcq), halves = min(2, q_boxes - 2 * qt);
-      mbar_arrive_expect_tx(q_full, 2 * halves * TQ::box_bytes(q_rows));
-      for (int h = 0; h < halves; ++h) {
-        const int box = 2 * qt + h, by = box / nx_q, x = s.x0 + (box - by * nx_q) * g.tcq, y = s.y0 + by * g.trq;
-        TQ::load(smem, h, &tm_q1, q_full, hk * g.group, x, y, s.b);
-        TQ::load(smem + TQ::BYTES, h, &tm_q2, q_full, hk * g.group, x, y, s.b);
+      const int nx_q = ceil_div(s.wq, g.tcq), copies = QUAD ? 4 : min(2, q_boxes - 2 * qt);
+      mbar_arrive_expect_tx(q_full, 2 * copies * TQ::box_bytes(q_rows));
+      for (int h = 0; h < copies; ++h) {
+        const int box = QUAD ? 0 : 2 * qt + h, by = box / nx_q, x = s.x0 + (box - by * nx_q) * g.tcq, y = s.y0 + by * g.trq;
+        TQ::load(smem, (QUAD ? 32 : 64) * h, &tm_q1, q_full, hk * g.group, x, y, s.b);
+        TQ::load(smem + TQ::BYTES, (QUAD ? 32 : 64) * h, &tm_q2, q_full, hk * g.group, x, y, s.b);
       }
       const uint32_t bytes = 2 * TK::box_bytes(kBK) + TV::box_bytes(kBK);
       int by = j0 / k_nx, bx = j0 - by * k_nx, issued = 0;
@@ -267,7 +272,7 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     const int gi = warp >> 2, m = gi & 1, p = gi >> 1;   // map and, with NP = 2, the parity of its tiles
     const int row = (warp & 3) * 32 + lane;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const DiffRow q = diff_query_row(g, s, 2 * qt + (row >> 6), row & 63);
+    const DiffRow q = QUAD ? diff_query_row(g, s, 0, lane) : diff_query_row(g, s, 2 * qt + (row >> 6), row & 63);
     const bool live = q.live;
     const int hq = hk * g.group + q.head;
     const int seen = live ? diff_visible(g, s, q.x) : 0x7FFFFFFF;   // of a sequence
@@ -282,29 +287,31 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       if (!ok) break;
       tc_fence_after();
       if (warp_live) {
-        uint32_t sv[2][32];
-        tmem_ld32(tS, sv[0]);
-        tmem_ld32(tS + 32, sv[1]);
+        constexpr int kChunk = QUAD ? 16 : 32, kChunks = QUAD ? 1 : 2;
+        uint32_t sv[kChunks][kChunk];
+#pragma unroll
+        for (int c = 0; c < kChunks; ++c) tmem_ld_cols<kChunk>(tS + (QUAD ? 16 * (warp & 3) : 32 * c), sv[c]);
         tmem_wait_ld();
         if (cut || g.causal) {
           const uint64_t mask = diff_seen(g, s, k_nx, j0 + j, seen);
           if (__any_sync(0xFFFFFFFFu, mask != ~0ull)) {
-            const uint32_t bits[2] = {static_cast<uint32_t>(mask), static_cast<uint32_t>(mask >> 32)};
+            const uint32_t bits[2] = {static_cast<uint32_t>(QUAD ? mask >> (16 * (warp & 3)) : mask), static_cast<uint32_t>(mask >> 32)};
 #pragma unroll
-            for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < kChunks; ++c)
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
+              for (int i = 0; i < kChunk; ++i)
                 if (!(bits[c] & (1u << i))) sv[c][i] = 0xFF800000u;
           }
         }
+        constexpr int kRun = kChunks * kChunk / 4;   // four chains
         float tops[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {   // four chains of eight
-          const uint32_t* x = &sv[c >> 1][16 * (c & 1)];
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t* x = &sv[c * kRun / kChunk][c * kRun % kChunk];
           float q = max3_nan(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
 #pragma unroll
-          for (int i = 3; i + 1 < 16; i += 2) q = max3_nan(q, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-          tops[c] = max_nan(q, __uint_as_float(x[15]));
+          for (int i = 3; i + 1 < kRun; i += 2) q = max3_nan(q, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+          tops[c] = max_nan(q, __uint_as_float(x[kRun - 1]));
         }
         const float top = max_nan(max3_nan(tops[0], tops[1], tops[2]), tops[3]) * sl2;
         // keep the reference unless the tile exceeds it by 2^8; a NaN score becomes the reference, and the row NaN
@@ -331,10 +338,10 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         const uint64_t scale2 = f2_pack(sl2, sl2), ref2 = f2_pack(-ref, -ref);
         uint64_t sum0 = f2_pack(l * alpha, 0.f), sum1 = f2_pack(0.f, 0.f);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t pk[16];
+        for (int c = 0; c < kChunks; ++c) {
+          uint32_t pk[kChunk / 2];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
+          for (int i = 0; i < kChunk / 2; ++i) {
             const uint64_t x = f2_fma(f2_pack(__uint_as_float(sv[c][2 * i]), __uint_as_float(sv[c][2 * i + 1])), scale2, ref2);
             float x0, x1, p0, p1;
             f2_unpack(x, x0, x1);
@@ -348,7 +355,16 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
             else sum0 = f2_add(sum0, f2_pack(p0, p1));
             pk[i] = diff_pack<F16>(p0, p1);
           }
-          tmem_st16(tS + 16 * c, pk);
+          if constexpr (QUAD) {
+            const uint32_t none[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if (k == (warp & 3)) tmem_st8(tS + 8 * k, pk);
+              else tmem_st8(tS + 8 * k, none);
+            }
+          } else {
+            tmem_st16(tS + 16 * c, pk);
+          }
         }
         float s0, s1;
         f2_unpack(f2_add(sum0, sum1), s0, s1);
@@ -389,8 +405,8 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
       const long long prow = a.part ? ((wide(s.b, g.kv_heads) + hk) * g.q_len + q.x) * g.group + q.head : 0;   // sequences only
       const long long prows = static_cast<long long>(g.batch) * g.q_heads * g.q_len;
       const int token = live ? s.token(q.x, q.y) : 0;
-      if (live && gi < 2 && a.part)
-        a.part[static_cast<long long>(a.splits) * prows * 2 * g.dv + (static_cast<long long>(sp) * prows + prow) * 2 + gi] = lse2[gi];
+      const long long part = (static_cast<long long>(sp) * prows + prow) * 2;
+      if (!QUAD && live && gi < 2 && a.part) a.part[static_cast<long long>(a.splits) * prows * 2 * g.dv + part + gi] = lse2[gi];
       if (live && gi < 2 && a.lse && !a.part)
         a.lse[((static_cast<long long>(gi) * g.batch + s.b) * g.q_heads + hq) * g.q_len + token] = lse2[gi] * kDiffLn2;
       const float lam = live ? diff_lambda<F16>(a.lam, g.lam_f32, hq) : 0.f;
@@ -415,8 +431,18 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
             }
           }
         if (!live || col >= g.dv) continue;
+        if constexpr (QUAD) {
+          // [quarter][row][2 DV], then log-sum-exps [2][quarter][row]: the tiles are free by now
+          float* w = reinterpret_cast<float*>(smem) + row * 2 * DV + col;
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 8; e += 4)
+              *reinterpret_cast<float4*>(w + i * DV + e) = make_float4(f[i][e], f[i][e + 1], f[i][e + 2], f[i][e + 3]);
+          continue;
+        }
         if (a.part) {
-          float* w = a.part + (static_cast<long long>(sp) * prows + prow) * 2 * g.dv + col;
+          float* w = a.part + part * g.dv + col;
 #pragma unroll
           for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -434,6 +460,33 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         *reinterpret_cast<uint4*>(o + col) = make_uint4(w[0], w[1], w[2], w[3]);
         if (o2) *reinterpret_cast<uint4*>(o2 + col) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
       }
+      if (QUAD && gi < 2) reinterpret_cast<float*>(smem)[128 * 2 * DV + gi * 128 + row] = lse2[gi];
+    }
+    if constexpr (QUAD) {
+      // the quarters' parts of a row into this split's
+      asm volatile("bar.sync 1, %0;" ::"n"(128 * NG) : "memory");
+      const int live_rows = s.wq * g.group, columns = 2 * g.dv;
+      const long long prows = static_cast<long long>(g.batch) * g.q_heads * g.q_len;
+      if (ok && *abort_flag == 0u)
+        for (int i = threadIdx.x; i < live_rows * columns; i += 128 * NG) {
+          const int rr = i / columns, c = i - rr * columns, m = c >= g.dv, cc = c - m * g.dv;
+          float l[4], top = -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) top = max_nan(top, l[k] = reinterpret_cast<const float*>(smem)[128 * 2 * DV + m * 128 + 32 * k + rr]);
+          const float ref = top == -INFINITY ? 0.f : top;
+          float sum = 0.f, v = 0.f;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float w = exp2f(l[k] - ref);
+            sum += w;
+            v = fmaf(w, reinterpret_cast<const float*>(smem)[(32 * k + rr) * 2 * DV + m * DV + cc], v);
+          }
+          const int t = diff_row_token(g, rr);
+          const long long prow = ((wide(s.b, g.kv_heads) + hk) * g.q_len + t) * g.group + rr - t * g.group;
+          const long long part = (static_cast<long long>(sp) * prows + prow) * 2;
+          a.part[part * g.dv + m * g.dv + cc] = sum == 0.f ? 0.f : v / sum;
+          if (cc == 0) a.part[static_cast<long long>(a.splits) * prows * 2 * g.dv + part + m] = sum == 0.f ? -INFINITY : ref + log2f(sum);
+        }
     }
   }
   tc_fence_before();
@@ -444,61 +497,75 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
   }
 }
 
-// The parts of a row over its key splits, weighted by their sums: a thread
-// owns eight columns of one (batch item, query head, token) row of both maps.
+// The parts of one (batch item, key head, token, head of the group) row over
+// its key splits, weighted by their sums: a CTA a row. Its threads are
+// 2 dv / 4 pieces of the two maps' outputs times groups that share the parts.
+constexpr int kJoinThreads = 256, kMostParts = 64;
 template <bool F16>
-__global__ void __launch_bounds__(256) diff_attn_join_kernel(const DiffFwdArgs a) {
+__global__ void __launch_bounds__(kJoinThreads) diff_attn_join_kernel(const DiffFwdArgs a) {
+  __shared__ float weight[2][kMostParts];
+  __shared__ float lse2[2];
+  __shared__ float4 sums[kJoinThreads];
   const DiffGeom& g = a.g;
-  const int pieces = g.dv / 8;
-  const long long prows = static_cast<long long>(g.batch) * g.q_heads * g.q_len;
-  const long long at = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const long long prow = at / pieces;
-  const int c = static_cast<int>(at - prow * pieces) * 8;
-  if (prow >= prows) return;
-  // rows are [batch][key head][token][head of the group]
+  const long long prows = static_cast<long long>(g.batch) * g.q_heads * g.q_len, prow = blockIdx.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (warp < 2) {
+    // warp m: weights of map m's parts
+    const float* l = a.part + static_cast<long long>(a.splits) * prows * 2 * g.dv + prow * 2 + warp;
+    float top = -INFINITY, sum = 0.f;
+    for (int s = lane; s < a.splits; s += 32) top = max_nan(top, weight[warp][s] = l[s * prows * 2]);
+    for (int o = 16; o > 0; o >>= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int s = lane; s < a.splits; s += 32) sum += weight[warp][s] = exp2f(weight[warp][s] - ref);
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    for (int s = lane; s < a.splits; s += 32) weight[warp][s] *= inv;
+    if (lane == 0) lse2[warp] = sum == 0.f ? -INFINITY : ref + log2f(sum);
+  }
+  __syncthreads();
+  const int pieces = g.dv / 2, groups = kJoinThreads / pieces, piece = threadIdx.x % pieces, gr = threadIdx.x / pieces;
+  if (gr < groups) {
+    const int m = piece >= g.dv / 4;
+    const float* p = a.part + prow * 2 * g.dv + piece * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = gr; s < a.splits; s += groups) {
+      const float4 v = *reinterpret_cast<const float4*>(p + s * prows * 2 * g.dv);
+      const float w = weight[m][s];
+      f.x = fmaf(w, v.x, f.x); f.y = fmaf(w, v.y, f.y); f.z = fmaf(w, v.z, f.z); f.w = fmaf(w, v.w, f.w);
+    }
+    sums[gr * pieces + piece] = f;
+  }
+  __syncthreads();
   const int gh = static_cast<int>(prow % g.group), t = static_cast<int>(prow / g.group % g.q_len);
   const int hk = static_cast<int>(prow / (static_cast<long long>(g.group) * g.q_len) % g.kv_heads);
   const int b = static_cast<int>(prow / (static_cast<long long>(g.group) * g.q_len * g.kv_heads));
   const int hq = hk * g.group + gh;
-  const float* sums = a.part + static_cast<long long>(a.splits) * prows * 2 * g.dv;
-  float f[2][8], lse2[2];
+  if (threadIdx.x < g.dv / 4) {
+    float f[2][4];
 #pragma unroll
-  for (int m = 0; m < 2; ++m) {
-    float top = -INFINITY;
-    for (int s = 0; s < a.splits; ++s) top = max_nan(top, sums[(s * prows + prow) * 2 + m]);
-    const float ref = top == -INFINITY ? 0.f : top;
-    float l = 0.f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[m][e] = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-      const float w = exp2f(sums[(s * prows + prow) * 2 + m] - ref);
-      const float4* p = reinterpret_cast<const float4*>(a.part + ((s * prows + prow) * 2 + m) * g.dv + c);
-      const float4 lo = p[0], hi = p[1];
-      l += w;
-      const float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[m][e] = fmaf(w, v[e], f[m][e]);
+    for (int m = 0; m < 2; ++m) {
+      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < groups; ++k) {
+        const float4 u = sums[k * pieces + m * (g.dv / 4) + threadIdx.x];
+        v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
+      }
+      f[m][0] = v.x; f[m][1] = v.y; f[m][2] = v.z; f[m][3] = v.w;
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    lse2[m] = l == 0.f ? -INFINITY : ref + log2f(l);
+    const float lam = diff_lambda<F16>(a.lam, g.lam_f32, hq);
+    uint32_t w[2], w2[2];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) f[m][e] *= inv;
+    for (int e = 0; e < 2; ++e) {
+      const float d0 = fmaf(-lam, f[1][2 * e], f[0][2 * e]), d1 = fmaf(-lam, f[1][2 * e + 1], f[0][2 * e + 1]);
+      w[e] = F16 ? pack_f16x2_sat(d0, d1) : pack_bf16x2(d0, d1);
+      w2[e] = F16 ? pack_f16x2_sat(f[1][2 * e], f[1][2 * e + 1]) : pack_bf16x2(f[1][2 * e], f[1][2 * e + 1]);
+    }
+    const long long to = b * g.o.b + wide(t, g.o.t) + wide(hq, g.o.h) + threadIdx.x * 4;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o) + to) = make_uint2(w[0], w[1]);
+    if (a.o2) *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.o2) + to) = make_uint2(w2[0], w2[1]);
   }
-  const float lam = diff_lambda<F16>(a.lam, g.lam_f32, hq);
-  uint32_t w[4], w2[4];
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float d0 = fmaf(-lam, f[1][2 * e], f[0][2 * e]), d1 = fmaf(-lam, f[1][2 * e + 1], f[0][2 * e + 1]);
-    w[e] = F16 ? pack_f16x2_sat(d0, d1) : pack_bf16x2(d0, d1);
-    w2[e] = F16 ? pack_f16x2_sat(f[1][2 * e], f[1][2 * e + 1]) : pack_bf16x2(f[1][2 * e], f[1][2 * e + 1]);
-  }
-  const long long to = b * g.o.b + wide(t, g.o.t) + wide(hq, g.o.h) + c;
-  *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o) + to) = make_uint4(w[0], w[1], w[2], w[3]);
-  if (a.o2) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.o2) + to) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
-  if (a.lse && c == 0)
-#pragma unroll
-    for (int m = 0; m < 2; ++m)
-      a.lse[((static_cast<long long>(m) * g.batch + b) * g.q_heads + hq) * g.q_len + t] = lse2[m] * kDiffLn2;
+  if (a.lse && threadIdx.x < 2)
+    a.lse[((static_cast<long long>(threadIdx.x) * g.batch + b) * g.q_heads + hq) * g.q_len + t] = lse2[threadIdx.x] * kDiffLn2;
 }
 
 template <int D, int DV, bool F16>
@@ -507,7 +574,7 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
   // Of 8 pairs, those on the FMA pipe: at dv <= 32 the softmax warps' own instructions bound too (window 64 map: 868 us
   // with none, 872 with two); at 64 and 128 two are best (128 -> 124 us, 140 -> 134 us)
   constexpr int POLY = DV <= 32 ? 0 : 2;
-  auto kernel = diff_attn_fwd_kernel<D, DV, F16, POLY>;
+  auto kernel = a.quad ? diff_attn_fwd_kernel<D, DV, F16, 0, true> : diff_attn_fwd_kernel<D, DV, F16, POLY, false>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Lay::ALLOC);
   if (e != cudaSuccess) return e;
   const DiffGeom& g = a.g;
@@ -523,22 +590,38 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
     return cudaErrorInvalidValue;
   kernel<<<static_cast<unsigned>(ctas), Lay::kThreads, Lay::ALLOC, stream>>>(q1, q2, k1, k2, v, a, q_tiles);
   if ((e = cudaGetLastError()) != cudaSuccess || !a.part) return e;
-  const long long threads = static_cast<long long>(a.g.batch) * a.g.q_heads * a.g.q_len * (a.g.dv / 8);
-  diff_attn_join_kernel<F16><<<static_cast<unsigned>((threads + 255) / 256), 256, 0, stream>>>(a);
+  const long long rows = static_cast<long long>(g.batch) * g.q_heads * g.q_len;   // few: the keys are split because they are
+  diff_attn_join_kernel<F16><<<static_cast<unsigned>(rows), kJoinThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }
 
 }  // namespace
 
-// Keys are split over CTAs when the query tiles alone leave most SMs idle: as
-// many splits as fill them, each of at least four tiles of keys.
+// CTAs that share a query tile's keys: the number with the least estimate of
+// (rounds of CTAs) x (boxes of one + 4 for its start and end), of four boxes at
+// least; + 3 for the launch that joins them. One CTA a tile of few rows counts
+// half as much again, since the form for few rows joins parts in any case.
+// Measured (16 x 8192 keys, 64 tiles): 65 us with two, 71 with four.
 int diff_splits(const DiffGeom& g) {
   if (g.window || g.q_len == 0 || g.batch == 0) return 1;
   const long long units = static_cast<long long>(g.batch) * g.kv_heads * ceil_div(diff_max_q_boxes(g), 2);
-  const long long tiles = (g.k_len + kBK - 1) / kBK;
-  const long long want = 2 * sm_count() / units, most = tiles / 4;
-  const long long s = want < most ? want : most;
-  return s > 1 ? static_cast<int>(s < 64 ? s : 64) : 1;
+  const int sms = sm_count(), boxes = ceil_div(g.k_len, kBK);
+  if (units >= 4ll * sms) return 1;
+  int best = 1;
+  float least = static_cast<float>((units + sms - 1) / sms) * (boxes + 4) * (diff_few_rows(g) ? 1.5f : 1.f);
+  for (int s = 2; s <= 64 && 4 * s <= boxes; ++s) {
+    const float cost = static_cast<float>((units * s + sms - 1) / sms) * (ceil_div(boxes, s) + 4) + 3;
+    if (cost < least) {
+      least = cost;
+      best = s;
+    }
+  }
+  return best;
+}
+
+size_t diff_split_bytes(const DiffGeom& g) {
+  const int s = diff_splits(g);
+  return s > 1 ? static_cast<size_t>(s) * g.batch * g.q_heads * g.q_len * 2 * (g.dv + 1) * sizeof(float) : 0;
 }
 
 bool diff_map(CUtensorMap* map, const DiffGeom& g, bool query, bool f16, const void* p, const DiffStrides& s, int e, int cols) {
@@ -556,11 +639,6 @@ bool diff_map(CUtensorMap* map, const DiffGeom& g, bool query, bool f16, const v
   const CUtensorMapSwizzle sw = cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : (cols == 32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B);
   return encode_tiled(map, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(p), dims, strides, box,
                       sw) == CUDA_SUCCESS;
-}
-
-size_t diff_split_bytes(const DiffGeom& g) {
-  const int s = diff_splits(g);
-  return s > 1 ? static_cast<size_t>(s) * g.batch * g.q_heads * g.q_len * 2 * (g.dv + 1) * sizeof(float) : 0;
 }
 
 cudaError_t launch_diff_attn_fwd(const DiffFwdArgs& a, bool f16, cudaStream_t stream) {
