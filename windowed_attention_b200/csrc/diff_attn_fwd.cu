@@ -599,18 +599,21 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
 
 // CTAs that share a query tile's keys: the number with the least estimate of
 // (rounds of CTAs) x (boxes of one + 4 for its start and end), of four boxes at
-// least; + 3 for the launch that joins them. One CTA a tile of few rows counts
-// half as much again, since the form for few rows joins parts in any case.
-// Measured (16 x 8192 keys, 64 tiles): 65 us with two, 71 with four.
+// least; + 3 for the launch that joins them. Full tiles write and read back as
+// much as four boxes more for each part, and are split only while they leave
+// SMs idle. One CTA a tile of few rows counts half as much again, since the
+// form for few rows joins parts in any case. Measured (16 x 8192 keys, 64 tiles
+// of 4 rows): 65 us with two, 71 with four.
 int diff_splits(const DiffGeom& g) {
   if (g.window || g.q_len == 0 || g.batch == 0) return 1;
+  const bool few = diff_few_rows(g);
   const long long units = static_cast<long long>(g.batch) * g.kv_heads * ceil_div(diff_max_q_boxes(g), 2);
-  const int sms = sm_count(), boxes = ceil_div(g.k_len, kBK);
-  if (units >= 4ll * sms) return 1;
+  const int sms = sm_count(), boxes = ceil_div(g.k_len, kBK), ends = few ? 4 : 8;
+  if (units >= (few ? 4ll : 1ll) * sms) return 1;
   int best = 1;
-  float least = static_cast<float>((units + sms - 1) / sms) * (boxes + 4) * (diff_few_rows(g) ? 1.5f : 1.f);
+  float least = static_cast<float>((units + sms - 1) / sms) * (boxes + 4) * (few ? 1.5f : 1.f);
   for (int s = 2; s <= 64 && 4 * s <= boxes; ++s) {
-    const float cost = static_cast<float>((units * s + sms - 1) / sms) * (ceil_div(boxes, s) + 4) + 3;
+    const float cost = static_cast<float>((units * s + sms - 1) / sms) * (ceil_div(boxes, s) + ends) + 3;
     if (cost < least) {
       least = cost;
       best = s;
