@@ -3,16 +3,19 @@
 // with the random bits of philox.cuh. The backward is the same call on the
 // upstream gradient.
 //
-// What bounds it: memory, 2 * n * size bytes (x once, y once). One thread owns
-// one Philox block of eight elements: 16 bytes of a 16-bit type, 32 of fp32.
-// A call of ten rounds is 20 wide multiplies and 20 three-input xors for eight
-// elements, under half of the issue slots that the memory time leaves.
+// What bounds it: the ten rounds. One thread owns Philox blocks of eight
+// elements: 16 bytes of a 16-bit type, 32 of fp32; a block takes 20 wide
+// multiplies and 20 three-input xors, and the selection works on word halves
+// without taking them apart. 41.5 M bf16 elements: 35.5 us, 0.71 of the time
+// that their 166 MB take at 6.54 TB/s (25 us); with one block a thread 39, with
+// four 37 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "philox.cuh"
 #include "rib_internal.h"
@@ -24,23 +27,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kBlocksPerThread = 2;   // Philox blocks of a thread, loaded before any is used
 
-template <typename T>
-__device__ __forceinline__ float to_f(T v);
-template <>
-__device__ __forceinline__ float to_f(float v) { return v; }
-template <>
-__device__ __forceinline__ float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-template <>
-__device__ __forceinline__ float to_f(__half v) { return __half2float(v); }
-template <typename T>
-__device__ __forceinline__ T from_f(float v);
-template <>
-__device__ __forceinline__ float from_f(float v) { return v; }
-template <>
-__device__ __forceinline__ __nv_bfloat16 from_f(float v) { return __float2bfloat16_rn(v); }
-template <>
-__device__ __forceinline__ __half from_f(float v) { return __float2half_rn(v); }
-
 // A dropped element is 0 whatever x holds (a selection, not a product).
 // x and y may be the same buffer: each element is read and written by one thread.
 template <typename T, bool VEC>
@@ -48,6 +34,9 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, siz
   constexpr int W = sizeof(T) * 8 / 16;   // 16-byte words of a block
   const uint64_t stream = rng.offset + (rng.step ? *rng.step : 0ull);
   const size_t blocks = (n + 7) / 8;
+  // thresholds up to 65535 in a word's high half; 65536 drops everything
+  const uint32_t least = rng.threshold << 16;
+  const bool all_dropped = rng.threshold > 65535u;
   const size_t first = static_cast<size_t>(blockIdx.x) * kThreads * kBlocksPerThread + threadIdx.x;
   union Pack {
     uint4 w[W];
@@ -63,7 +52,7 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, siz
       for (int i = 0; i < W; ++i) in[k].w[i] = reinterpret_cast<const uint4*>(x + b * 8)[i];
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) in[k].e[i] = b * 8 + i < n ? x[b * 8 + i] : from_f<T>(0.f);
+      for (int i = 0; i < 8; ++i) in[k].e[i] = b * 8 + i < n ? x[b * 8 + i] : T(0.f);
     }
   }
 #pragma unroll
@@ -71,10 +60,34 @@ __global__ void __launch_bounds__(kThreads) dropout_kernel(const T* x, T* y, siz
     const size_t b = first + static_cast<size_t>(k) * kThreads;
     if (b >= blocks) continue;
     const uint4 bits = philox4x32_10(b, stream, rng.seed);
+    const uint32_t words[4] = {bits.x, bits.y, bits.z, bits.w};
     Pack out;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      out.e[i] = from_f<T>(drop_bits(bits, i) >= rng.threshold ? to_f(in[k].e[i]) * rng.up : 0.f);
+    for (int i = 0; i < 4; ++i) {
+      // elements 2 i and 2 i + 1 own the low and the high half of a word; both are compared in the high half's place
+      const bool low = (words[i] << 16) >= least, high = words[i] >= least;
+      if constexpr (sizeof(T) == 4) {
+        out.e[2 * i] = low ? in[k].e[2 * i] * rng.up : T(0);
+        out.e[2 * i + 1] = high ? in[k].e[2 * i + 1] * rng.up : T(0);
+      } else {
+        const uint32_t v = reinterpret_cast<const uint32_t*>(in[k].w)[i];
+        const uint64_t up = f2_pack(rng.up, rng.up);
+        float a, c;
+        uint32_t r;
+        if constexpr (std::is_same<T, __half>::value) {
+          f2_unpack(f2_mul(f2_pack(f16_lo(v), f16_hi(v)), up), a, c);
+          const __half2 h = __floats2half2_rn(a, c);
+          r = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+          f2_unpack(f2_mul(f2_pack(bf16_lo(v), bf16_hi(v)), up), a, c);
+          r = pack_bf16x2(a, c);
+        }
+        reinterpret_cast<uint32_t*>(out.w)[i] = (low ? r & 0xFFFFu : 0u) | (high ? r & 0xFFFF0000u : 0u);
+      }
+    }
+    if (all_dropped)
+#pragma unroll
+      for (int i = 0; i < W; ++i) out.w[i] = make_uint4(0u, 0u, 0u, 0u);
     if (VEC && b * 8 + 8 <= n) {
 #pragma unroll
       for (int i = 0; i < W; ++i) reinterpret_cast<uint4*>(y + b * 8)[i] = out.w[i];

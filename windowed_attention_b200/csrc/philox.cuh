@@ -39,10 +39,4 @@ __device__ __forceinline__ uint4 philox4x32_10(uint64_t block, uint64_t stream, 
   return make_uint4(c0, c1, c2, c3);
 }
 
-// The 16 bits of element e (0..7) of a block.
-__device__ __forceinline__ uint32_t drop_bits(const uint4& w, int e) {
-  const uint32_t v = e < 4 ? (e < 2 ? w.x : w.y) : (e < 6 ? w.z : w.w);
-  return (e & 1) ? v >> 16 : v & 0xFFFFu;
-}
-
 }  // namespace rib
