@@ -222,6 +222,63 @@ def test_single_tokens_over_long_keys(cuda_lib, G, t):
     _check(cuda_lib, 1, 4, 9000, G, 1, 16, 32, t, causal=True, rms=("o",))
 
 
+@pytest.mark.parametrize("Nq,G,Nk", [(6, 5, 3000), (32, 1, 2000), (3, 10, 5000), (2, 16, 1300), (33, 1, 4000)])
+def test_few_rows_over_split_keys(cuda_lib, Nq, G, Nk):
+    """Up to 32 rows a key head stand in every lane quarter; 33 do not. With the backward."""
+    _check(cuda_lib, 1, Nq, Nk, G, 1, 32, 64, BF16, rms=("o", "o2", "dv"))
+    _check(cuda_lib, 2, Nq, Nk, 2 * G, 2, 16, 32, F16, lens=[Nk - 77, 70], causal=True)
+
+
+def test_many_heads_on_one_key_head(cuda_lib):
+    _check(cuda_lib, 1, 70, 70, 64, 1, 16, 32, BF16, causal=True)
+    _check(cuda_lib, 1, 90, 90, 33, 1, 32, 64, BF16)
+
+
+@pytest.mark.parametrize("H,W,window", [(26, 29, 12), (20, 40, 31), (16, 16, 8)])
+def test_a_bad_window_stays_in_its_window(cuda_lib, H, W, window):
+    """NaN in every tensor of one window: the others' results are the same bits."""
+    t, N = BF16, H * W
+    x = _inputs(1, N, N, 2, 1, 16, 32, t)
+    one = _run(cuda_lib, x, 0.25, t, window=window, width=W)
+    bad = torch.zeros(H, W, dtype=torch.bool, device="cuda")
+    bad[window:2 * window, :window] = True
+    bad = bad.reshape(-1)
+    for k in NAMES + ("do",):
+        x[k][0, bad] = float("nan")
+    two = _run(cuda_lib, x, 0.25, t, window=window, width=W)
+    for k in ("o", "o2", "dq1", "dq2", "dk1", "dk2", "dv"):
+        assert torch.equal(one[k][0, ~bad], two[k][0, ~bad]), k
+        assert torch.isnan(two[k][0, bad]).all(), k
+    assert torch.equal(one["lse"][..., ~bad], two["lse"][..., ~bad])
+
+
+def test_two_calls_at_once(cuda_lib):
+    """Two streams, each with its own outputs and workspace."""
+    rib, t = cuda_lib, BF16
+    xs = [_inputs(1, 700, 700, 4, 2, 32, 64, t, seed=s) for s in (1, 2)]
+    want = [_run(rib, x, 0.2, t, causal=True) for x in xs]
+    desc = rib.diff_attn_desc(1, 700, 700, 4, 2, 32, 64, 0.2, t, causal=True)
+    streams, outs, keep = [torch.cuda.Stream() for _ in xs], [], []
+    torch.cuda.synchronize()
+    for x, st in zip(xs, streams):
+        out = {k: torch.full_like(v, float("nan")) for k, v in want[0].items()}
+        ws = torch.empty(max(1, rib.rib_diff_attention_workspace_size(desc)), dtype=torch.uint8, device="cuda")
+        wb = torch.empty(rib.rib_diff_attention_bwd_workspace_size(desc), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        outs.append(out)
+        keep.append((ws, wb))
+    for _ in range(3):
+        for x, st, out, (ws, wb) in zip(xs, streams, outs, keep):
+            args = [x[k] for k in NAMES + ("lam",)] + [None]
+            rib.rib_diff_attention(desc, *args, out["o"], out["o2"], out["lse"], ws, stream=st)
+            rib.rib_diff_attention_bwd(desc, *args, out["o"], out["o2"], out["lse"], x["do"], *(out["d" + k] for k in NAMES + ("lam",)), wb,
+                                       stream=st)
+    torch.cuda.synchronize()
+    for w, out in zip(want, outs):
+        for k in w:
+            assert torch.equal(w[k], out[k]), k
+
+
 def test_long_sequences(cuda_lib):
     _check(cuda_lib, 1, 4500, 4500, 2, 1, 64, 128, BF16, causal=True, rms=ALL)
     _check(cuda_lib, 1, 6000, 6000, 1, 1, 16, 32, F16, rms=ALL)
