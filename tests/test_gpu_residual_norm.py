@@ -97,7 +97,7 @@ def _check(rib, T, C, xt, t, pre, post, gated, groups, p, rpg=None, **kw):
             _near(got["d" + k], g["d" + k], F32, (chain * 2.0 ** -24 + K * 8) * g[f"d{k}_abs"] + K * big * 1e-3, "d" + k)
 
 
-SHAPES = [(1, 1), (3, 2), (5, 7), (2, 8), (33, 48), (64, 180), (257, 180), (19, 255), (130, 256), (40, 1021), (21, 1024), (9, 2050),
+SHAPES = [(1, 1), (4, 1), (17, 3), (300, 33), (65, 510), (31, 511), (12, 2045), (10, 2047), (9, 3001), (3, 2), (5, 7), (2, 8), (33, 48), (64, 180), (257, 180), (19, 255), (130, 256), (40, 1021), (21, 1024), (9, 2050),
           (6, 4095), (7, 4096)]
 
 

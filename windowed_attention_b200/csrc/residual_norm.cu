@@ -78,6 +78,9 @@ __device__ __forceinline__ void load_v(const void* base, uint32_t at, float (&f)
     if constexpr (V == 4) {
       const float4 v = *reinterpret_cast<const float4*>(p);
       f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w;
+    } else if constexpr (V == 2) {
+      const float2 v = *reinterpret_cast<const float2*>(p);
+      f[0] = v.x; f[1] = v.y;
     } else {
       f[0] = *reinterpret_cast<const float*>(p);
     }
@@ -89,18 +92,45 @@ __device__ __forceinline__ void load_v(const void* base, uint32_t at, float (&f)
       f[1] = kHalf ? f16_hi(v.x) : bf16_hi(v.x);
       f[2] = kHalf ? f16_lo(v.y) : bf16_lo(v.y);
       f[3] = kHalf ? f16_hi(v.y) : bf16_hi(v.y);
+    } else if constexpr (V == 2) {
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(p);
+      f[0] = kHalf ? f16_lo(v) : bf16_lo(v);
+      f[1] = kHalf ? f16_hi(v) : bf16_hi(v);
     } else {
       const uint32_t v = *reinterpret_cast<const uint16_t*>(p);
       f[0] = kHalf ? f16_lo(v) : bf16_lo(v);
     }
   }
 }
-// The same where `in`, else zeros.
+// Which of a thread's V elements lie in the row: all or none, but for pairs (V
+// == 2) of odd rows, which start one element early so that they are aligned.
+template <int V>
+struct Inside {
+  bool all;
+  __device__ __forceinline__ bool operator[](int) const { return all; }
+  __device__ __forceinline__ bool any() const { return all; }
+};
+template <>
+struct Inside<2> {
+  bool lo, hi;
+  __device__ __forceinline__ bool operator[](int e) const { return e ? hi : lo; }
+  __device__ __forceinline__ bool any() const { return lo || hi; }
+};
+template <int V>
+__device__ __forceinline__ Inside<V> inside(bool live, int c, int C) {
+  if constexpr (V == 2) return {live && c >= 0 && c < C, live && c + 1 < C};
+  else return {live && c < C};
+}
+// Elements from a stage or the weights beside it, zeros where they are not in the row.
 template <typename T, int V>
-__device__ __forceinline__ void load_if(const T* base, uint32_t at, bool in, float (&f)[V]) {
+__device__ __forceinline__ void load_if(const T* base, uint32_t at, const Inside<V>& in, float (&f)[V]) {
 #pragma unroll
   for (int e = 0; e < V; ++e) f[e] = 0.f;
-  if (in) load_v<T, V>(base, at, f);
+  if (in.any()) load_v<T, V>(base, at, f);
+  if constexpr (V == 2) {
+    if (!in.lo) f[0] = 0.f;
+    if (!in.hi) f[1] = 0.f;
+  }
 }
 // SAT: fp16 results beyond +-65504 saturate, as in every forward store of the
 // library. Gradients do not: an overflow has to stay visible to loss scaling.
@@ -109,6 +139,7 @@ __device__ __forceinline__ void store_v(void* base, uint32_t at, const float (&f
   T* p = static_cast<T*>(base) + at;
   if constexpr (sizeof(T) == 4) {
     if constexpr (V == 4) *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    else if constexpr (V == 2) *reinterpret_cast<float2*>(p) = make_float2(f[0], f[1]);
     else *reinterpret_cast<float*>(p) = f[0];
   } else {
     constexpr bool kHalf = std::is_same<T, __half>::value;
@@ -123,7 +154,23 @@ __device__ __forceinline__ void store_v(void* base, uint32_t at, const float (&f
       }
     };
     if constexpr (V == 4) *reinterpret_cast<uint2*>(p) = make_uint2(pack(f[0], f[1]), pack(f[2], f[3]));
+    else if constexpr (V == 2) *reinterpret_cast<uint32_t*>(p) = pack(f[0], f[1]);
     else *reinterpret_cast<uint16_t*>(p) = static_cast<uint16_t>(pack(f[0], 0.f));
+  }
+}
+
+template <typename T, int V, bool SAT>
+__device__ __forceinline__ void store_if(T* base, uint32_t at, const Inside<V>& in, const float (&f)[V]) {
+  if constexpr (V == 2) {
+    if (in.lo && in.hi) {
+      store_v<T, 2, SAT>(base, at, f);
+    } else {   // the pair's other element is a neighbouring row's
+      const float lo[1] = {f[0]}, hi[1] = {f[1]};
+      if (in.lo) store_v<T, 1, SAT>(base, at, lo);
+      if (in.hi) store_v<T, 1, SAT>(base, at + 1, hi);
+    }
+  } else {
+    if (in.all) store_v<T, V, SAT>(base, at, f);
   }
 }
 
@@ -255,15 +302,22 @@ __device__ __forceinline__ void drop_factor(const DropRng& rng, uint64_t stream,
     m[2] = (b & 0xFFFFu) >= rng.threshold ? rng.up : 0.f;
     m[3] = (b >> 16) >= rng.threshold ? rng.up : 0.f;
   } else {
+    const auto half = [](const uint4& w, uint32_t s) {
+      const uint32_t v = s < 4 ? (s < 2 ? w.x : w.y) : (s < 6 ? w.z : w.w);
+      return (s & 1) ? v >> 16 : v & 0xFFFFu;
+    };
     const uint32_t s = static_cast<uint32_t>(at & 7);
-    const uint32_t v = s < 4 ? (s < 2 ? w.x : w.y) : (s < 6 ? w.z : w.w);
-    m[0] = ((s & 1) ? v >> 16 : v & 0xFFFFu) >= rng.threshold ? rng.up : 0.f;
+    m[0] = half(w, s) >= rng.threshold ? rng.up : 0.f;
+    if constexpr (V == 2) {
+      const uint4 next = s == 7 ? philox4x32_10((at >> 3) + 1, stream, rng.seed) : w;
+      m[1] = half(next, (s + 1) & 7) >= rng.threshold ? rng.up : 0.f;
+    }
   }
 }
 
 // v := (v - mean) * r in place; returns r. Elements behind the row's end stay 0.
 template <int V, int NV, bool WIDE>
-__device__ __forceinline__ float normalise(float (&v)[NV][V], const bool (&in)[NV], int kind, const NormParams& p, int lpr,
+__device__ __forceinline__ float normalise(float (&v)[NV][V], const Inside<V> (&in)[NV], int kind, const NormParams& p, int lpr,
                                            float (*red)[2][32], int& phase) {
   float s[1];
   if (kind == 1) {
@@ -277,7 +331,7 @@ __device__ __forceinline__ float normalise(float (&v)[NV][V], const bool (&in)[N
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[k][e] = in[k] ? v[k][e] - mean : 0.f;
+      for (int e = 0; e < V; ++e) v[k][e] = in[k][e] ? v[k][e] - mean : 0.f;
   }
   s[0] = 0.f;
 #pragma unroll
@@ -296,6 +350,16 @@ __device__ __forceinline__ float normalise(float (&v)[NV][V], const bool (&in)[N
 __device__ __forceinline__ long long group_of(long long row, long long per) {
   if (((row | per) >> 32) == 0) return static_cast<uint32_t>(row) / static_cast<uint32_t>(per);
   return row / per;
+}
+
+// Columns of a CTA's weight arrays in shared memory; pairs keep a second copy of
+// them, shifted by one element for the rows that start on an odd one.
+__host__ __device__ inline int weight_columns(int C) { return (C + 1 + 3) / 4 * 4; }
+template <int V>
+__device__ __forceinline__ void put_weight(float* weights, int arrays, int which, int c, int C, float v) {
+  const int wide = weight_columns(C);
+  weights[which * wide + c] = v;
+  if constexpr (V == 2) weights[(arrays + which) * wide + c + 1] = v;
 }
 
 // One row per group of lpr threads, CTAs walking blocks of rows.
@@ -326,15 +390,19 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
   int st = 0;
   // the weights of every column, in shared memory: post_w, post_b, pre_w, pre_b, scale (of the first group)
   float* weights = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
-  const int wide_c = (p.C + 3) / 4 * 4;
+  const int wide_c = weight_columns(p.C);
   for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-    weights[c] = p.post_w ? p.post_w[c] : 1.f;
-    weights[wide_c + c] = p.post_b ? p.post_b[c] : 0.f;
-    weights[2 * wide_c + c] = p.pre_w ? p.pre_w[c] : 1.f;
-    weights[3 * wide_c + c] = p.pre_b ? p.pre_b[c] : 0.f;
-    weights[4 * wide_c + c] = p.scale ? p.scale[c] : 1.f;
+    put_weight<V>(weights, 5, 0, c, p.C, p.post_w ? p.post_w[c] : 1.f);
+    put_weight<V>(weights, 5, 1, c, p.C, p.post_b ? p.post_b[c] : 0.f);
+    put_weight<V>(weights, 5, 2, c, p.C, p.pre_w ? p.pre_w[c] : 1.f);
+    put_weight<V>(weights, 5, 3, c, p.C, p.pre_b ? p.pre_b[c] : 0.f);
+    put_weight<V>(weights, 5, 4, c, p.C, p.scale ? p.scale[c] : 1.f);
   }
   const bool many = p.scale && p.rows_per_group < p.T;   // groups
+  // pairs: this thread's rows all start on an even element of their block (par 0) or all on an odd one, since the CTA's
+  // rows in step are an even number
+  const int par = V == 2 && (p.C & 1) ? slot & 1 : 0;
+  const float* w0 = weights + (par ? 5 * wide_c : 0) + lane * V;
   for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
     const long long r0 = b * p.block, r1 = last(b), next = b + gridDim.x;
     if (p.stages == 2 && next < blocks) io.start(st ^ 1, next * p.block, last(next), src);
@@ -343,22 +411,21 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
     for (int rr = slot; rr - slot < p.block; rr += rows_per_cta) {
       const long long row = r0 + rr;
       const bool live = row < r1;
-      const uint32_t at = (live ? rr * p.C : 0) + lane * V;
+      const uint32_t at = (live ? rr : par) * p.C + lane * V - par;
       XT* sx = reinterpret_cast<XT*>(stage + p.off[kX]) + at;
       YT* sy = reinterpret_cast<YT*>(stage + p.off[kY]) + at;
       const YT* sg = reinterpret_cast<const YT*>(stage + p.off[kG]) + at;
-      bool in[NV];
+      Inside<V> in[NV];
       float x[NV][V], u[NV][V];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        in[k] = live && (lane + k * lpr) * V < p.C;
+        in[k] = inside<V>(live, (lane + k * lpr) * V - par, p.C);
         load_if<XT, V>(sx, k * lpr * V, in[k], x[k]);
       }
       if (p.y) {
 #pragma unroll
         for (int k = 0; k < NV; ++k) load_if<YT, V>(sy, k * lpr * V, in[k], u[k]);
         if (p.post) normalise<V, NV, WIDE>(u, in, p.post, p, lpr, red, phase);
-        const float* w0 = weights + lane * V;
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           float w[V], c[V];
@@ -367,13 +434,21 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
 #pragma unroll
           for (int e = 0; e < V; ++e) u[k][e] = fmaf(u[k][e], w[e], c[e]);
         }
-        const float* scale = many && live ? p.scale + group_of(row, p.rows_per_group) * p.C + lane * V : w0 + 4 * wide_c;
+        if (many) {
+          const float* scale = p.scale + (live ? group_of(row, p.rows_per_group) : 0) * p.C;
 #pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          float w[V];
-          load_if<float, V>(scale, k * lpr * V, in[k], w);
+          for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) u[k][e] *= w[e];
+            for (int e = 0; e < V; ++e)
+              if (in[k][e]) u[k][e] *= scale[(lane + k * lpr) * V - par + e];
+        } else {
+#pragma unroll
+          for (int k = 0; k < NV; ++k) {
+            float w[V];
+            load_if<float, V>(w0, 4 * wide_c + k * lpr * V, in[k], w);
+#pragma unroll
+            for (int e = 0; e < V; ++e) u[k][e] *= w[e];
+          }
         }
         if (p.gate) {
 #pragma unroll
@@ -388,7 +463,7 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
 #pragma unroll
           for (int k = 0; k < NV; ++k) {
             float m[V];
-            drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V, m);
+            drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V - par, m);
             // a dropped element adds 0 whatever the branch holds
 #pragma unroll
             for (int e = 0; e < V; ++e) u[k][e] = m[e] != 0.f ? m[e] * u[k][e] : 0.f;
@@ -397,22 +472,22 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] = in[k] ? x[k][e] + u[k][e] : 0.f;
+          for (int e = 0; e < V; ++e) x[k][e] = in[k][e] ? x[k][e] + u[k][e] : 0.f;
         if (p.x_out)
 #pragma unroll
           for (int k = 0; k < NV; ++k)
-            if (in[k]) store_v<XT, V, true>(sx, k * lpr * V, x[k]);
+            store_if<XT, V, true>(sx, k * lpr * V, in[k], x[k]);
       }
       if (p.pre) {
         normalise<V, NV, WIDE>(x, in, p.pre, p, lpr, red, phase);
 #pragma unroll
         for (int k = 0; k < NV; ++k) {
           float w[V], c[V];
-          load_if<float, V>(weights + lane * V, 2 * wide_c + k * lpr * V, in[k], w);
-          load_if<float, V>(weights + lane * V, 3 * wide_c + k * lpr * V, in[k], c);
+          load_if<float, V>(w0, 2 * wide_c + k * lpr * V, in[k], w);
+          load_if<float, V>(w0, 3 * wide_c + k * lpr * V, in[k], c);
 #pragma unroll
           for (int e = 0; e < V; ++e) x[k][e] = fmaf(x[k][e], w[e], c[e]);
-          if (in[k]) store_v<YT, V, true>(sy, k * lpr * V, x[k]);
+          store_if<YT, V, true>(sy, k * lpr * V, in[k], x[k]);
         }
       }
     }
@@ -467,13 +542,15 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
   if (first < behind) io.start(0, lo(first), hi(first), src);
   // the weights of every column, in shared memory: pre_w, post_w, post_b, scale
   float* weights = reinterpret_cast<float*>(smem + p.stages * p.stage_bytes);
-  const int wide_c = (p.C + 3) / 4 * 4;
+  const int wide_c = weight_columns(p.C);
   for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
-    weights[c] = p.pre_w ? p.pre_w[c] : 1.f;
-    weights[wide_c + c] = p.post_w ? p.post_w[c] : 1.f;
-    weights[2 * wide_c + c] = p.post_b ? p.post_b[c] : 0.f;
-    weights[3 * wide_c + c] = scale ? scale[c] : 1.f;
+    put_weight<V>(weights, 4, 0, c, p.C, p.pre_w ? p.pre_w[c] : 1.f);
+    put_weight<V>(weights, 4, 1, c, p.C, p.post_w ? p.post_w[c] : 1.f);
+    put_weight<V>(weights, 4, 2, c, p.C, p.post_b ? p.post_b[c] : 0.f);
+    put_weight<V>(weights, 4, 3, c, p.C, scale ? scale[c] : 1.f);
   }
+  const int par = V == 2 && (p.C & 1) ? slot & 1 : 0;   // as in the forward
+  const float* w0 = weights + (par ? 4 * wide_c : 0) + lane * V;
   int st = 0;
   for (long long blk = first; blk < behind; ++blk) {
     const long long r0 = lo(blk), r1 = hi(blk);
@@ -484,19 +561,18 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
     for (int rr = slot; rr - slot < p.block; rr += rows_per_cta) {
       const long long row = r0 + rr;
       const bool live = row < r1;
-      const uint32_t at = (live ? rr * p.C : 0) + lane * V;
+      const uint32_t at = (live ? rr : par) * p.C + lane * V - par;
       XT* sx = reinterpret_cast<XT*>(stage + p.off[kX]) + at;
       XT* sd = reinterpret_cast<XT*>(stage + p.off[kD]) + at;
       YT* sy = reinterpret_cast<YT*>(stage + p.off[kY]) + at;
       YT* sg = reinterpret_cast<YT*>(stage + p.off[kG]) + at;
       const YT* sh = reinterpret_cast<const YT*>(stage + p.off[kH]) + at;
-      const float* w0 = weights + lane * V;
-      bool in[NV];
+      Inside<V> in[NV];
       float d[NV][V];
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        in[k] = live && (lane + k * lpr) * V < p.C;
-        load_if<XT, V>(sd, k * lpr * V, in[k] && p.dx_out, d[k]);
+        in[k] = inside<V>(live, (lane + k * lpr) * V - par, p.C);
+        load_if<XT, V>(sd, k * lpr * V, inside<V>(live && p.dx_out, (lane + k * lpr) * V - par, p.C), d[k]);
       }
       if (pre) {
         float xh[NV][V], dh[NV][V];
@@ -525,13 +601,13 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) d[k][e] = in[k] ? fmaf(r, dh[k][e] - m0 - xh[k][e] * m1, d[k][e]) : 0.f;
+          for (int e = 0; e < V; ++e) d[k][e] = in[k][e] ? fmaf(r, dh[k][e] - m0 - xh[k][e] * m1, d[k][e]) : 0.f;
       }
       if (p.dx) {
         XT* out = pre ? sx : sd;
 #pragma unroll
         for (int k = 0; k < NV; ++k)
-          if (in[k]) store_v<XT, V, false>(out, k * lpr * V, d[k]);
+          store_if<XT, V, false>(out, k * lpr * V, in[k], d[k]);
       }
       if (!p.y) continue;
       float u[NV][V];
@@ -549,7 +625,7 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
 #pragma unroll
         for (int e = 0; e < V; ++e) m[e] = g[e] = 1.f;
         if (p.gate) load_if<YT, V>(sg, k * lpr * V, in[k], g);
-        if (p.rng.threshold) drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V, m);
+        if (p.rng.threshold) drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V - par, m);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
           const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
@@ -564,7 +640,7 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
           s[0] += d[k][e];
           s[1] = fmaf(d[k][e], u[k][e], s[1]);
         }
-        if (in[k] && p.dgate) store_v<YT, V, false>(sg, k * lpr * V, dg);
+        if (p.dgate) store_if<YT, V, false>(sg, k * lpr * V, in[k], dg);
       }
       if (!p.dy) continue;
       if (p.post) {
@@ -577,7 +653,7 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
       }
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (in[k]) store_v<YT, V, false>(sy, k * lpr * V, d[k]);
+        store_if<YT, V, false>(sy, k * lpr * V, in[k], d[k]);
     }
     io.finish(st, r0, r1, dst, held);
     if (p.stages == 2) st ^= 1;
@@ -587,19 +663,19 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
 
   // the CTA's groups of threads, one sum at a time, in their order
   if (!p.partial) return;
-  float* acc_smem = reinterpret_cast<float*>(smem);   // [slots][lpr * NV * V], one sum at a time
-  const int width = lpr * NV * V;
+  float* acc_smem = reinterpret_cast<float*>(smem);   // [slots][lpr * NV * V + 1], one sum at a time, column c at c + 1
+  const int width = lpr * NV * V + 1;
 #pragma unroll
   for (int s = 0; s < kSums; ++s) {
     __syncthreads();
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) acc_smem[slot * width + (lane + k * lpr) * V + e] = acc[s][k][e];
+      for (int e = 0; e < V; ++e) acc_smem[slot * width + (lane + k * lpr) * V + e - par + 1] = acc[s][k][e];
     __syncthreads();
     for (int c = threadIdx.x; c < p.C; c += blockDim.x) {
       float v = 0.f;
-      for (int q = 0; q < rows_per_cta; ++q) v += acc_smem[q * width + c];
+      for (int q = 0; q < rows_per_cta; ++q) v += acc_smem[q * width + c + 1];
       p.partial[(static_cast<size_t>(blockIdx.x) * kSums + s) * p.C + c] = v;
     }
   }
@@ -636,31 +712,37 @@ __global__ void __launch_bounds__(256) residual_norm_sum_kernel(const NormSums p
 
 // The threads of a row and the vectors of a thread: the fewest slots that hold
 // C, and among equals rows inside a warp (no barriers), then more threads.
+// Vectors of four where C % 4 == 0 and the tensors are aligned; pairs else,
+// which odd rows start one element early (see Inside); single elements for odd
+// rows too wide for two of them in step.
 struct RowShape {
   int v, nv, lpr_log2;
 };
-RowShape row_shape(int C, bool vec, int max_nv) {
-  RowShape best{vec ? 4 : 1, 0, 0};
+RowShape row_shape(int C, bool vec) {
+  const bool odd_wide = C % 2 && C > 2046;
+  RowShape best{vec ? 4 : (odd_wide ? 1 : 2), 0, 0};
   long best_slots = 1L << 60;
-  const int vecs = vec ? C / 4 : C;
-  const int options4[] = {1, 2, 3}, options1[] = {4, 8, 8};
+  const int vecs = vec ? C / 4 : (odd_wide ? C : (C % 2 ? C / 2 + 1 : C / 2));
+  const int options4[] = {1, 2, 3}, options2[] = {1, 2, 4}, options1[] = {8, 8, 8};
+  const int* options = vec ? options4 : (odd_wide ? options1 : options2);
   const int order[] = {5, 4, 3, 2, 6, 7, 8, 9};
-  for (int l : order)
-    for (int i = 0; i < (vec ? max_nv : 2); ++i) {
-      const int nv = vec ? options4[i] : options1[i];
-      const long slots = static_cast<long>(nv) << l;
+  for (int l : order) {
+    if (best.v == 2 && C % 2 && l > 8) continue;   // two rows of 256 threads in step at least
+    for (int i = 0; i < 3; ++i) {
+      const long slots = static_cast<long>(options[i]) << l;
       if (slots >= vecs && slots < best_slots) {
         best_slots = slots;
-        best.nv = nv;
+        best.nv = options[i];
         best.lpr_log2 = l;
       }
     }
+  }
   return best;
 }
 
-// Threads of a CTA: 512 for rows of 512 threads, and where a block's shared
+// Threads of a CTA: 512 for rows of 256 threads or more, and where a block's shared
 // memory leaves room for no more than two CTAs an SM.
-int cta_threads(int lpr_log2, long long block_bytes) { return lpr_log2 > 8 || block_bytes > 56 * 1024 ? 512 : 256; }
+int cta_threads(int lpr_log2, long long block_bytes) { return lpr_log2 > 7 || block_bytes > 56 * 1024 ? 512 : 256; }
 // Rows that make whole 16-byte pieces of a tensor of that element size.
 int row_unit(int C, int size) {
   int unit = 1;
@@ -710,11 +792,12 @@ cudaError_t allow_smem(K kernel, int bytes) {
 
 template <typename XT, typename YT>
 cudaError_t launch_fwd(NormParams p, bool vec, bool aligned, cudaStream_t stream) {
-  const RowShape s = row_shape(p.C, vec, 3);
+  const RowShape s = row_shape(p.C, vec);
   const int threads = cta_threads(s.lpr_log2, static_cast<long long>(row_unit(p.C, sizeof(YT))) * p.C * (sizeof(XT) + 2 * sizeof(YT)));
+  const int weights = (s.v == 2 ? 10 : 5) * weight_columns(p.C) * static_cast<int>(sizeof(float));
   const int rows_per_cta = threads >> s.lpr_log2;
-  plan_blocks(&p, {p.x, nullptr, p.y, p.gate, nullptr}, {true, false, true, false, false}, sizeof(XT), sizeof(YT), rows_per_cta, aligned, 20 * p.C + 80);
-  const int smem = p.stages * p.stage_bytes + 20 * ((p.C + 3) / 4 * 4);
+  plan_blocks(&p, {p.x, nullptr, p.y, p.gate, nullptr}, {true, false, true, false, false}, sizeof(XT), sizeof(YT), rows_per_cta, aligned, weights);
+  const int smem = p.stages * p.stage_bytes + weights;
   const long long blocks = (p.T + p.block - 1) / p.block;
   const int by_smem = 227 * 1024 / (smem + 2048), by_threads = 1024 / threads;
   const long long most = static_cast<long long>(sm_count()) * (by_smem < by_threads ? by_smem : by_threads);
@@ -729,23 +812,28 @@ cudaError_t launch_fwd(NormParams p, bool vec, bool aligned, cudaStream_t stream
 #define RIB_FWD(V, NV)                                                                     \
   if (s.v == V && s.nv == NV) return wide ? run(residual_norm_fwd_kernel<XT, YT, V, NV, true>) \
                                           : run(residual_norm_fwd_kernel<XT, YT, V, NV, false>);
-  RIB_FWD(4, 1) RIB_FWD(4, 2) RIB_FWD(4, 3) RIB_FWD(1, 4) RIB_FWD(1, 8)
+  RIB_FWD(4, 1) RIB_FWD(4, 2) RIB_FWD(4, 3) RIB_FWD(2, 1) RIB_FWD(2, 2) RIB_FWD(2, 4) RIB_FWD(1, 8)
 #undef RIB_FWD
   return cudaErrorInvalidConfiguration;
 }
 
 template <typename XT, typename YT>
-cudaError_t launch_bwd(NormParams p, bool vec, bool aligned, int groups, cudaStream_t stream) {
-  const RowShape s = row_shape(p.C, vec, 3);
+cudaError_t launch_bwd(NormParams p, bool vec, bool aligned, int groups, int* chunks, cudaStream_t stream) {
+  const RowShape s = row_shape(p.C, vec);
   const int threads = cta_threads(s.lpr_log2, static_cast<long long>(row_unit(p.C, sizeof(YT))) * p.C * (2 * sizeof(XT) + 3 * sizeof(YT)));
+  const int weights = (s.v == 2 ? 8 : 4) * weight_columns(p.C) * static_cast<int>(sizeof(float));
   const int rows_per_cta = threads >> s.lpr_log2;
   const bool pre = p.pre != 0;
   plan_blocks(&p, {pre ? p.x : nullptr, p.dx_out, p.y, p.gate, pre ? p.dh : nullptr}, {false, false, false, false, false}, sizeof(XT),
-              sizeof(YT), rows_per_cta, aligned, 16 * p.C + 64);
-  p.chunks = static_cast<int>(bwd_chunks(p.T, p.rows_per_group, groups));
+              sizeof(YT), rows_per_cta, aligned, weights);
+  const int sums = p.partial ? rows_per_cta * ((s.v * s.nv << s.lpr_log2) + 1) * static_cast<int>(sizeof(float)) : 0;
+  const int stages = p.stages * p.stage_bytes + weights, smem = stages > sums ? stages : sums;
+  // the CTAs that run at once, in whole chunks a group, and no more than the workspace's partials
+  const int by_smem = 227 * 1024 / (smem + 2048), per_sm = by_smem < 512 / threads ? by_smem : 512 / threads;
+  const long long most = bwd_chunks(p.T, p.rows_per_group, groups), fit = static_cast<long long>(sm_count()) * (per_sm > 0 ? per_sm : 1) / groups;
+  p.chunks = static_cast<int>(fit < 1 ? 1 : (fit < most ? fit : most));
+  *chunks = p.chunks;
   const unsigned grid = static_cast<unsigned>(p.chunks) * groups;
-  const int sums = p.partial ? rows_per_cta * (s.v * s.nv << s.lpr_log2) * static_cast<int>(sizeof(float)) : 0;
-  const int stages = p.stages * p.stage_bytes + 16 * ((p.C + 3) / 4 * 4), smem = stages > sums ? stages : sums;
   const bool wide = s.lpr_log2 > 5;
   const auto run = [&](auto kernel) {
     const cudaError_t e = allow_smem(kernel, smem);
@@ -756,7 +844,7 @@ cudaError_t launch_bwd(NormParams p, bool vec, bool aligned, int groups, cudaStr
 #define RIB_BWD(V, NV)                                                                     \
   if (s.v == V && s.nv == NV) return wide ? run(residual_norm_bwd_kernel<XT, YT, V, NV, true>) \
                                           : run(residual_norm_bwd_kernel<XT, YT, V, NV, false>);
-  RIB_BWD(4, 1) RIB_BWD(4, 2) RIB_BWD(4, 3) RIB_BWD(1, 4) RIB_BWD(1, 8)
+  RIB_BWD(4, 1) RIB_BWD(4, 2) RIB_BWD(4, 3) RIB_BWD(2, 1) RIB_BWD(2, 2) RIB_BWD(2, 4) RIB_BWD(1, 8)
 #undef RIB_BWD
   return cudaErrorInvalidConfiguration;
 }
@@ -901,13 +989,12 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_
     if (!(p.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
     make_drop_rng(d->p, d->seed, d->offset, step, &p.rng);
     const bool vec = a.vec && d->C % 4 == 0;
-    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, groups, stream);
-    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, t.bulk, groups, stream);
-    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, t.bulk, groups, stream);
-    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, t.bulk, groups, stream);
-    else e = launch_bwd<float, float>(p, vec, t.bulk, groups, stream);
+    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, groups, &sp.chunks, stream);
+    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, t.bulk, groups, &sp.chunks, stream);
+    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, t.bulk, groups, &sp.chunks, stream);
+    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, t.bulk, groups, &sp.chunks, stream);
+    else e = launch_bwd<float, float>(p, vec, t.bulk, groups, &sp.chunks, stream);
     if (e != cudaSuccess) return cuda_fail(e, "rib_residual_norm_bwd launch");
-    sp.chunks = static_cast<int>(bwd_chunks(d->T, d->rows_per_group, groups));
   }
   if (!sums) return RIB_OK;
   // no rows: the sums are empty and the gradients zero
