@@ -107,19 +107,28 @@ __device__ __forceinline__ void load_v(const void* base, uint32_t at, float (&f)
 template <int V>
 struct Inside {
   bool all;
+  float f;   // 1 or 0
+  __device__ __forceinline__ float one(int) const { return f; }
   __device__ __forceinline__ bool operator[](int) const { return all; }
   __device__ __forceinline__ bool any() const { return all; }
 };
 template <>
 struct Inside<2> {
   bool lo, hi;
+  float f[2];
+  __device__ __forceinline__ float one(int e) const { return f[e]; }
   __device__ __forceinline__ bool operator[](int e) const { return e ? hi : lo; }
   __device__ __forceinline__ bool any() const { return lo || hi; }
 };
 template <int V>
 __device__ __forceinline__ Inside<V> inside(bool live, int c, int C) {
-  if constexpr (V == 2) return {live && c >= 0 && c < C, live && c + 1 < C};
-  else return {live && c < C};
+  if constexpr (V == 2) {
+    const bool lo = live && c >= 0 && c < C, hi = live && c + 1 < C;
+    return {lo, hi, {lo ? 1.f : 0.f, hi ? 1.f : 0.f}};
+  } else {
+    const bool all = live && c < C;
+    return {all, all ? 1.f : 0.f};
+  }
 }
 // Elements from a stage or the weights beside it, zeros where they are not in the row.
 template <typename T, int V>
@@ -331,7 +340,7 @@ __device__ __forceinline__ float normalise(float (&v)[NV][V], const Inside<V> (&
 #pragma unroll
     for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int e = 0; e < V; ++e) v[k][e] = in[k][e] ? v[k][e] - mean : 0.f;
+      for (int e = 0; e < V; ++e) v[k][e] = fmaf(-mean, in[k].one(e), v[k][e]);   // stays 0 outside the row
   }
   s[0] = 0.f;
 #pragma unroll
@@ -472,7 +481,7 @@ __global__ void __launch_bounds__(512, 2) residual_norm_fwd_kernel(const __grid_
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) x[k][e] = in[k][e] ? x[k][e] + u[k][e] : 0.f;
+          for (int e = 0; e < V; ++e) x[k][e] += u[k][e];
         if (p.x_out)
 #pragma unroll
           for (int k = 0; k < NV; ++k)
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
-          for (int e = 0; e < V; ++e) d[k][e] = in[k][e] ? fmaf(r, dh[k][e] - m0 - xh[k][e] * m1, d[k][e]) : 0.f;
+          for (int e = 0; e < V; ++e) d[k][e] = fmaf(r, fmaf(-m1, xh[k][e], fmaf(-m0, in[k].one(e), dh[k][e])), d[k][e]);
       }
       if (p.dx) {
         XT* out = pre ? sx : sd;
@@ -623,22 +632,31 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
         load_if<float, V>(w0, 2 * wide_c + k * lpr * V, in[k], b);
         load_if<float, V>(w0, 3 * wide_c + k * lpr * V, in[k], sc);
 #pragma unroll
-        for (int e = 0; e < V; ++e) m[e] = g[e] = 1.f;
+        for (int e = 0; e < V; ++e) g[e] = 1.f;
         if (p.gate) load_if<YT, V>(sg, k * lpr * V, in[k], g);
-        if (p.rng.threshold) drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V - par, m);
+        const auto branch = [&](auto drops) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) {
-          const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
-          const float dm = m[e] != 0.f ? d[k][e] * m[e] : 0.f;
-          const float dmu = m[e] != 0.f ? dm * uu : 0.f;
-          dg[e] = dmu * sc[e];
-          acc[0][k][e] = fmaf(dmu, g[e], acc[0][k][e]);
-          const float du = dm * sc[e] * g[e];
-          acc[1][k][e] = fmaf(du, u[k][e], acc[1][k][e]);
-          acc[2][k][e] += du;
-          d[k][e] = du * w[e];
-          s[0] += d[k][e];
-          s[1] = fmaf(d[k][e], u[k][e], s[1]);
+          for (int e = 0; e < V; ++e) {
+            const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
+            // a dropped element has no part in any gradient, whatever the branch holds
+            const bool kept = !decltype(drops)::value || m[e] != 0.f;
+            const float dm = kept ? (decltype(drops)::value ? d[k][e] * m[e] : d[k][e]) : 0.f;
+            const float dmu = kept ? dm * uu : 0.f;
+            dg[e] = dmu * sc[e];
+            acc[0][k][e] = fmaf(dmu, g[e], acc[0][k][e]);
+            const float du = dm * (sc[e] * g[e]);
+            acc[1][k][e] = fmaf(du, u[k][e], acc[1][k][e]);
+            acc[2][k][e] += du;
+            d[k][e] = du * w[e];
+            s[0] += d[k][e];
+            s[1] = fmaf(d[k][e], u[k][e], s[1]);
+          }
+        };
+        if (p.rng.threshold) {
+          drop_factor<V>(p.rng, stream, static_cast<uint64_t>(row) * p.C + (lane + k * lpr) * V - par, m);
+          branch(std::true_type{});
+        } else {
+          branch(std::false_type{});
         }
         if (p.dgate) store_if<YT, V, false>(sg, k * lpr * V, in[k], dg);
       }
