@@ -465,8 +465,7 @@ typedef struct {
  * x_out NULL: x' is not stored. h goes with pre != RIB_NORM_NONE. x_out may be
  * x, and h may be y. h is taken from x' before x' is rounded to x_dtype. fp16
  * results saturate at +-65504. T == 0 launches nothing. Tensors need their
- * element's alignment; with C % 4 == 0 and every tensor aligned to four
- * elements the rows move as vectors. */
+ * element's alignment; at 16 bytes the rows move by bulk copies. */
 rib_status rib_residual_norm(const rib_residual_norm_desc* desc, const void* x, const void* y, const void* gate,
                              const float* scale, const float* post_w, const float* post_b, const float* pre_w,
                              const float* pre_b, void* x_out, void* h, const uint64_t* step, cudaStream_t stream);
@@ -524,7 +523,7 @@ typedef struct {
  * as parts that a second kernel joins: workspace >=
  * rib_diff_attention_workspace_size() bytes (0 otherwise; NULL then). Tensors
  * and workspace 16-byte aligned. A row whose scores hold a NaN or an infinity
- * becomes NaN. */
+ * becomes NaN. Outputs may not overlap inputs. */
 size_t rib_diff_attention_workspace_size(const rib_diff_attn_desc* desc);
 rib_status rib_diff_attention(const rib_diff_attn_desc* desc, const void* q1, const void* q2, const void* k1, const void* k2,
                               const void* v, const void* lam, const int* k_lens, void* o, void* o2, float* lse,

@@ -12,7 +12,7 @@
 //   du = dx' f gate,  dpost_w = sum du y^,  dpost_b = sum du, dy from du post_w,
 //   dpre_w = sum dh x'^,  dpre_b = sum dh.
 //
-// What bounds both: memory. Each tensor is read or written once. A CTA walks
+// Memory is the floor of both: each tensor is read or written once. A CTA walks
 // blocks of whole rows, which are contiguous in every tensor: bulk copies
 // bring a block into shared memory while the block before is computed, results
 // overwrite their inputs there and leave by bulk copies, so no thread waits for
@@ -22,6 +22,11 @@
 // each thread NV vectors of V elements), statistics are two passes over those
 // registers (mean, then squared deviations: no cancellation), and the backward
 // recomputes them from x' and y rather than reading saved ones.
+//
+// Measured: 640x360 rows of 180, fp32 stream, bf16 branch and gate, forward 112
+// us (581 MB, 5.2 TB/s); 16x96x96 rows of 180 with dropout, forward 105 and
+// backward 193 us (floors 57 and 89); 4039 rows of 1021 in fp16, 48 and 81 us
+// (floors 9 and 14). What is above the floors is instruction issue.
 //
 // Column sums (weights, scale) of the backward: every thread keeps its own
 // columns' sums in fp32 registers over the rows that its group walks; the
