@@ -131,7 +131,7 @@ __device__ __forceinline__ uint64_t diff_key_mask(const DiffGeom& g, int vx, int
 __device__ __forceinline__ uint64_t diff_seen(const DiffGeom& g, const DiffSeq& s, int nx, int j, int seen) {
   if (g.window) {
     const DiffKeyBox k = diff_key_box(g, s, nx, j);
-    return diff_key_mask(g, k.vx, k.vy);
+    return k.vx >= g.tck && k.vy >= g.trk ? ~0ull : diff_key_mask(g, k.vx, k.vy);
   }
   const int left = seen - 64 * j;
   return left >= 64 ? ~0ull : (left > 0 ? (1ull << left) - 1ull : 0ull);
@@ -177,6 +177,18 @@ struct DiffTile {
     for (int c = lane; c < D / 8; c += lanes) *reinterpret_cast<uint4*>(tile + offset(row, c)) = make_uint4(0u, 0u, 0u, 0u);
   }
 };
+
+// Zeros into the rows of a box whose bits are set, two tiles of width D and one of DV behind them, by a warp.
+template <int ROWS, int D, int DV>
+__device__ __forceinline__ void diff_clear_rows(uint8_t* tiles, uint64_t rows, int lane) {
+  while (rows) {
+    const int row = __ffsll(static_cast<long long>(rows)) - 1;
+    rows &= rows - 1;
+    DiffTile<ROWS, D>::clear_row(tiles, row, lane, 32);
+    DiffTile<ROWS, D>::clear_row(tiles + DiffTile<ROWS, D>::BYTES, row, lane, 32);
+    DiffTile<ROWS, DV>::clear_row(tiles + 2 * DiffTile<ROWS, D>::BYTES, row, lane, 32);
+  }
+}
 
 __host__ __device__ constexpr uint32_t diff_idesc(bool f16, int N, bool b_mn) {
   return f16 ? idesc_f16(128, N, false, b_mn) : idesc_bf16(128, N, false, b_mn);

@@ -278,12 +278,7 @@ diff_attn_dq_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_cons
         const uint64_t mask = diff_key_mask(g, k.vx, k.vy);
         uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
         if (mask != ~0ull) {
-          for (int row = 0; row < kStream; ++row)
-            if (!((mask >> row) & 1ull)) {
-              TK::clear_row(to, row, lane, 32);
-              TK::clear_row(to + TK::BYTES, row, lane, 32);
-              TV::clear_row(to + 2 * TK::BYTES, row, lane, 32);
-            }
+          diff_clear_rows<kStream, D, DV>(to, ~mask, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
@@ -643,12 +638,15 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         const int by = (j0 + i) / q_nx, vx = s.wq - (j0 + i - by * q_nx) * g.tcq, vy = s.hq - by * g.trq;
         uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
         if (vx < g.tcq || vy < g.trq) {
-          for (int row = 0; row < q_rows; ++row)
-            if (!diff_query_row(g, s, j0 + i, row).live) {
-              TQ::clear_row(to, row, lane, 32);
-              TQ::clear_row(to + TQ::BYTES, row, lane, 32);
-              TO::clear_row(to + 2 * TQ::BYTES, row, lane, 32);
-            }
+          // rows that the load brought and that are not the window's
+          uint64_t dead = 0ull;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int row = 32 * h + lane;
+            const uint32_t bits = __ballot_sync(0xFFFFFFFFu, row < q_rows && !diff_query_row(g, s, j0 + i, row).live);
+            dead |= static_cast<uint64_t>(bits) << (32 * h);
+          }
+          diff_clear_rows<kStream, D, DV>(to, dead, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();

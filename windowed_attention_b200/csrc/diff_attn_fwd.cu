@@ -201,12 +201,7 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
         const uint64_t mask = diff_key_mask(g, k.vx, k.vy);
         uint8_t* to = smem + Lay::OFF_ST + st * Lay::STAGE;
         if (mask != ~0ull) {
-          for (int row = 0; row < kBK; ++row)
-            if (!((mask >> row) & 1ull)) {
-              TK::clear_row(to, row, lane, 32);
-              TK::clear_row(to + TK::BYTES, row, lane, 32);
-              TV::clear_row(to + 2 * TK::BYTES, row, lane, 32);
-            }
+          diff_clear_rows<kBK, D, DV>(to, ~mask, lane);
           fence_proxy_async_smem();
         }
         __syncwarp();
