@@ -198,3 +198,18 @@ def test_diff_attention_binding_refusals():
         rib.diff_attn_desc(1, 4, 4, 2, 2, 16, 32, 0.25, torch.int32)
     with pytest.raises(ValueError):
         _lib._strided_arg("q1", t, (1, 4, 2, 16), None, d.dtype, 0)
+
+
+def test_diff_attention_layout_follows_descriptor():
+    # one descriptor used again after its fields change: the checks see the new sizes, strides and types
+    d = rib.diff_attn_desc(1, 4, 6, 2, 1, 16, 32, 0.25, torch.bfloat16)
+    first = _lib._diff_layout(d)
+    assert first[1:] == (((1, 4, 2, 16), None), ((1, 6, 1, 16), None), ((1, 6, 1, 32), None), ((1, 4, 2, 32), None), d.dtype, d.lam_dtype, 2, 1, 16)
+    assert _lib._diff_layout(d) is first
+    d.q_len = 9
+    d.q_stride[0], d.q_stride[1], d.q_stride[2] = 576, 64, 32
+    d.dtype += 1
+    now = _lib._diff_layout(d)
+    assert now[1] == ((1, 9, 2, 16), (576, 64, 32)) and now[4] == ((1, 9, 2, 32), None) and now[5] == d.dtype and now[-1] == 36
+    d.q_stride[1] = 96
+    assert _lib._diff_layout(d)[1][1] == (576, 96, 32)

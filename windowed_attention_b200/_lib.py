@@ -542,11 +542,6 @@ def _strided_arg(name, t, shape, strides, desc_code, device) -> Optional[int]:
     return t.data_ptr()
 
 
-def _strides_of(field):
-    s = tuple(field)
-    return s if any(s) else None
-
-
 def _workspace_arg(ws, device):
     if ws is None:
         return None, 0
@@ -556,19 +551,23 @@ def _workspace_arg(ws, device):
     return (ws.data_ptr() if n else None), n
 
 
-def _diff_args(d, dev):
-    """Checkers of the query, key, value and output tensors of a descriptor."""
-    b, nq, nk, hq, hk, e, ev, code = d.batch, d.q_len, d.k_len, d.q_heads, d.kv_heads, d.d, d.dv, d.dtype
-    q, k, v, o = (b, nq, hq, e), (b, nk, hk, e), (b, nk, hk, ev), (b, nq, hq, ev)
-    sq, sk, sv, so = _strides_of(d.q_stride), _strides_of(d.k_stride), _strides_of(d.v_stride), _strides_of(d.o_stride)
-    return (lambda n, t: _strided_arg(n, t, q, sq, code, dev), lambda n, t: _strided_arg(n, t, k, sk, code, dev),
-            lambda n, t: _strided_arg(n, t, v, sv, code, dev), lambda n, t: _strided_arg(n, t, o, so, code, dev))
+def _diff_layout(d):
+    """Shapes and strides (None: contiguous) of the query, key, value and
+    output tensors of a descriptor: kept on it for as long as its bytes stay."""
+    key = bytes(d)
+    kept = getattr(d, "_layout", None)
+    if kept is None or kept[0] != key:
+        b, nq, nk, hq, hk, e, ev = d.batch, d.q_len, d.k_len, d.q_heads, d.kv_heads, d.d, d.dv
+        st = [tuple(f) if any(f) else None for f in (d.q_stride, d.k_stride, d.v_stride, d.o_stride)]
+        kept = d._layout = (key, ((b, nq, hq, e), st[0]), ((b, nk, hk, e), st[1]), ((b, nk, hk, ev), st[2]), ((b, nq, hq, ev), st[3]),
+                            d.dtype, d.lam_dtype, hq, b, 2 * b * hq * nq)
+    return kept
 
 
 def _lens_arg(k_lens, batch, device) -> Optional[int]:
-    import torch
     if k_lens is None:
         return None
+    import torch
     if k_lens.dtype != torch.int32 or k_lens.numel() < batch or k_lens.get_device() != device or not k_lens.is_contiguous():
         raise ValueError("k_lens holds one int32 a batch item on the current device")
     return k_lens.data_ptr()
@@ -583,12 +582,14 @@ def rib_diff_attention(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens=None, 
     """o = (softmax(scale q1 k1^T) - lam softmax(scale q2 k2^T)) v; o2 and lse
     (None for inference) are what the backward needs (see include/rib.h)."""
     load()
-    dev, d = _current_device(q1), desc
-    qa, ka, va, oa = _diff_args(d, dev)
+    dev = _current_device(q1)
+    _, (qs, qt), (ks, kt), (vs, vt), (os, ot), code, lam_code, heads, batch, rows = _diff_layout(desc)
+    arg = _strided_arg
     _check(_lib.rib_diff_attention(
-        ctypes.byref(d), qa("q1", q1), qa("q2", q2), ka("k1", k1), ka("k2", k2), va("v", v), _arg("lam", lam, d.q_heads, d.lam_dtype, dev),
-        _lens_arg(k_lens, d.batch, dev), oa("o", o), oa("o2", o2),
-        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), *_workspace_arg(workspace, dev), _stream(stream)))
+        ctypes.byref(desc), arg("q1", q1, qs, qt, code, dev), arg("q2", q2, qs, qt, code, dev), arg("k1", k1, ks, kt, code, dev),
+        arg("k2", k2, ks, kt, code, dev), arg("v", v, vs, vt, code, dev), _arg("lam", lam, heads, lam_code, dev),
+        _lens_arg(k_lens, batch, dev), arg("o", o, os, ot, code, dev), arg("o2", o2, os, ot, code, dev), _arg("lse", lse, rows, RIB_F32, dev),
+        *_workspace_arg(workspace, dev), _stream(stream)))
 
 
 def rib_diff_attention_bwd_workspace_size(desc: DiffAttnDesc) -> int:
@@ -600,10 +601,13 @@ def rib_diff_attention_bwd(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens, o
     """Every gradient of rib_diff_attention from do and the forward's o, o2 and
     lse (see include/rib.h)."""
     load()
-    dev, d = _current_device(q1), desc
-    qa, ka, va, oa = _diff_args(d, dev)
+    dev = _current_device(q1)
+    _, (qs, qt), (ks, kt), (vs, vt), (os, ot), code, lam_code, heads, batch, rows = _diff_layout(desc)
+    arg = _strided_arg
     _check(_lib.rib_diff_attention_bwd(
-        ctypes.byref(d), qa("q1", q1), qa("q2", q2), ka("k1", k1), ka("k2", k2), va("v", v), _arg("lam", lam, d.q_heads, d.lam_dtype, dev),
-        _lens_arg(k_lens, d.batch, dev), oa("o", o), oa("o2", o2),
-        _arg("lse", lse, 2 * d.batch * d.q_heads * d.q_len, RIB_F32, dev), oa("do", do), qa("dq1", dq1), qa("dq2", dq2), ka("dk1", dk1),
-        ka("dk2", dk2), va("dv", dv), _arg("dlam", dlam, d.q_heads, d.lam_dtype, dev), *_workspace_arg(workspace, dev), _stream(stream)))
+        ctypes.byref(desc), arg("q1", q1, qs, qt, code, dev), arg("q2", q2, qs, qt, code, dev), arg("k1", k1, ks, kt, code, dev),
+        arg("k2", k2, ks, kt, code, dev), arg("v", v, vs, vt, code, dev), _arg("lam", lam, heads, lam_code, dev),
+        _lens_arg(k_lens, batch, dev), arg("o", o, os, ot, code, dev), arg("o2", o2, os, ot, code, dev), _arg("lse", lse, rows, RIB_F32, dev),
+        arg("do", do, os, ot, code, dev), arg("dq1", dq1, qs, qt, code, dev), arg("dq2", dq2, qs, qt, code, dev),
+        arg("dk1", dk1, ks, kt, code, dev), arg("dk2", dk2, ks, kt, code, dev), arg("dv", dv, vs, vt, code, dev),
+        _arg("dlam", dlam, heads, lam_code, dev), *_workspace_arg(workspace, dev), _stream(stream)))
