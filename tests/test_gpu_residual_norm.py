@@ -8,6 +8,9 @@ weights) covers the chains here (a lane adds at most 8-12 terms, then 9
 levels of a tree, twice, and about 20 products). Column sums add T terms in
 chains of at most `chain` additions, each off by 2^-24 of the running sum,
 which is at most the sum of magnitudes, plus K units for each term."""
+import ctypes
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -288,3 +291,45 @@ def test_step_reaches_the_join(cuda_lib):
     two = _run(cuda_lib, a, T, C, F32, BF16, "layer", "layer", T, 0.2, offset=2, step=step)
     for k in one:
         assert torch.equal(one[k], two[k]), k
+
+
+def test_two_host_threads(cuda_lib):
+    """Host threads run joins of two widths of one kernel instance, whose shared memory differs, on their own streams:
+    every call is accepted, and its results are those of a call alone."""
+    rib, T = cuda_lib, 2
+    lib, jobs = rib.load(), []
+    for C in (2048, 4092, 2048, 4092):
+        g = torch.Generator().manual_seed(C)
+        x, y, gate = torch.randn(T, C, generator=g).cuda(), *(torch.randn(T, C, generator=g).to(BF16).cuda() for _ in range(2))
+        desc = rib.residual_norm_desc(T, C, F32, BF16, pre="layer", post="layer", eps=EPS)
+        alone, out = ([torch.empty_like(t) for t in (x, y, x, y)] for _ in range(2))
+        rib.rib_residual_norm(desc, x, y, gate, x_out=alone[0], h=alone[1])
+        rib.rib_residual_norm_bwd(desc, alone[0], y, gate, dx_out=x, dh=y, dx=alone[2], dy=alone[3])
+        jobs.append((desc, x, y, gate, alone, out, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(jobs))
+
+    def work(desc, x, y, gate, alone, out, stream, failed):
+        # arguments made once: most of a thread's time is spent inside the library, without the interpreter's lock
+        p, c = (lambda t: None if t is None else ctypes.c_void_p(t.data_ptr())), ctypes.byref(desc)
+        st, x1 = ctypes.c_void_p(stream.cuda_stream), out[0]
+        fwd = [p(t) for t in (x, y, gate, None, None, None, None, None, x1, out[1], None)]
+        bwd = [p(t) for t in (x1, y, gate, None, None, None, None, x, y, out[2], out[3], *[None] * 6)]
+        torch.cuda.set_device(0)
+        start.wait()
+        for _ in range(8000):
+            if lib.rib_residual_norm(c, *fwd, st) or lib.rib_residual_norm_bwd(c, *bwd, None, 0, None, st):
+                failed.append(lib.rib_last_error().decode())
+                return
+
+    threads = [threading.Thread(target=work, args=j) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    rib.rib_device_error()
+    for desc, _, _, _, alone, out, _, failed in jobs:
+        assert not failed, failed
+        for a, b in zip(alone, out):
+            assert torch.equal(a, b), desc.C

@@ -784,7 +784,7 @@ long long bwd_chunks(long long T, long long rows_per_group, int groups) {
 // multiples of 16 bytes, that is 8 / gcd(C, 8) rows of a 16-bit tensor. Blocks
 // of about 24 KB in two stages leave room for two to four CTAs an SM; wide
 // rows get what fits, in one stage.
-constexpr int kSmemMost = 224 * 1024;
+constexpr int kSmemMost = 224 * 1024;   // of any plan of C <= kMaxC, weights included
 void plan_blocks(NormParams* p, const void* const (&src)[5], const bool (&held)[5], int xs, int ys, int rows_per_cta, bool aligned, int extra) {
   int elem = 0;
   for (int i = 0; i < 5; ++i)
@@ -807,10 +807,13 @@ void plan_blocks(NormParams* p, const void* const (&src)[5], const bool (&held)[
   p->stages = p->bulk && 2 * p->stage_bytes + extra <= kSmemMost / 2 ? 2 : 1;
 }
 
-// Beyond 48 KB, static arrays included, a kernel has to ask.
+// Beyond 48 KB, static arrays included, a kernel has to ask. The limit belongs to
+// the kernel, not to the call, and one instance serves many sizes: it is always
+// raised to the most that any plan takes, so that a call of another host thread
+// cannot lower it between this call's request and its launch.
 template <typename K>
 cudaError_t allow_smem(K kernel, int bytes) {
-  return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) : cudaSuccess;
+  return bytes > 46 * 1024 ? cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) : cudaSuccess;
 }
 
 template <typename XT, typename YT>
