@@ -333,3 +333,24 @@ def test_two_host_threads(cuda_lib):
         assert not failed, failed
         for a, b in zip(alone, out):
             assert torch.equal(a, b), desc.C
+
+
+@pytest.mark.parametrize("C", [64, 37, 2050])
+@pytest.mark.parametrize("post", ["none", "layer"])
+def test_dropped_elements_have_no_gradient(cuda_lib, C, post):
+    """Infinities and NaN in the branch (without a post norm), the gate and the scale of dropped elements change nothing, to
+    the bit; the gradients are the oracle's."""
+    T, p = 24, 0.5
+    a = _make(T, C, F32, BF16, "layer", post, True, T)
+    dropped = torch.from_numpy(bo.dropout_factor(T * C, p, 11, 5) == 0).view(T, C)
+    bad = {k: v if v is None else v.clone() for k, v in a.items()}
+    for i, k in enumerate(("gate", "scale") + (("y",) if post == "none" else ())):
+        for j, v in enumerate((float("nan"), float("inf"), -float("inf"))):
+            bad[k][dropped & ((torch.arange(T) + i)[:, None] % 3 == j)] = v
+    args = (T, C, F32, BF16, "layer", post, 1, p)
+    want, got = _run(cuda_lib, a, *args), _run(cuda_lib, bad, *args)
+    for k, v in want.items():
+        if v is not None:
+            assert torch.isfinite(v).all(), k
+            assert torch.equal(v, got[k]), f"{k}: {int((v != got[k]).sum())} of {v.numel()} differ"
+    _check(cuda_lib, T, C, F32, BF16, "layer", post, True, T, p, rpg=1)

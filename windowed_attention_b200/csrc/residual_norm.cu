@@ -643,13 +643,16 @@ __global__ void __launch_bounds__(512) residual_norm_bwd_kernel(const __grid_con
 #pragma unroll
           for (int e = 0; e < V; ++e) {
             const float uu = fmaf(u[k][e], w[e], b[e]);   // N_post(y) post_w + post_b
-            // a dropped element has no part in any gradient, whatever the branch holds
+            // a dropped element has no part in any gradient, whatever the branch, the gate and the scale hold there
             const bool kept = !decltype(drops)::value || m[e] != 0.f;
-            const float dm = kept ? (decltype(drops)::value ? d[k][e] * m[e] : d[k][e]) : 0.f;
-            const float dmu = kept ? dm * uu : 0.f;
-            dg[e] = dmu * sc[e];
-            acc[0][k][e] = fmaf(dmu, g[e], acc[0][k][e]);
-            const float du = dm * (sc[e] * g[e]);
+            float du = 0.f;
+            dg[e] = 0.f;
+            if (kept) {
+              const float dm = decltype(drops)::value ? d[k][e] * m[e] : d[k][e], dmu = dm * uu;
+              dg[e] = dmu * sc[e];
+              acc[0][k][e] = fmaf(dmu, g[e], acc[0][k][e]);
+              du = dm * (sc[e] * g[e]);
+            }
             acc[1][k][e] = fmaf(du, u[k][e], acc[1][k][e]);
             acc[2][k][e] += du;
             d[k][e] = du * w[e];
