@@ -534,7 +534,10 @@ rib_status rib_diff_attention(const rib_diff_attn_desc* desc, const void* q1, co
  * behind a length are 0, those of a shared key head sums over its query heads.
  * Probabilities and score gradients take dtype for the products (fp16 ones are
  * held times 64: an |P (dP - D)| above 1023 becomes infinite, which loss
- * scaling looks for). Deterministic: the same bits on every run. workspace >=
+ * scaling looks for). D is formed from the stored o, o2 and dO, whose rounding
+ * it takes over. scale >= 2^-100, in fp16 2^-26; a row of fp16 with |lse| / scale
+ * of 2.1e9 or more (scores of that size before the scale) makes the gradients of
+ * its keys NaN. Deterministic: the same bits on every run. workspace >=
  * rib_diff_attention_bwd_workspace_size() bytes, 16-byte aligned. */
 size_t rib_diff_attention_bwd_workspace_size(const rib_diff_attn_desc* desc);
 rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* desc, const void* q1, const void* q2, const void* k1, const void* k2,

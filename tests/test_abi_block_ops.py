@@ -213,3 +213,10 @@ def test_diff_attention_layout_follows_descriptor():
     assert now[1] == ((1, 9, 2, 16), (576, 64, 32)) and now[4] == ((1, 9, 2, 32), None) and now[5] == d.dtype and now[-1] == 36
     d.q_stride[1] = 96
     assert _lib._diff_layout(d)[1][1] == (576, 96, 32)
+
+
+def test_diff_attention_backward_scale_range(lib):
+    # below it the row constants of the backward leave the 16-bit type; refused before any pointer is used
+    for dtype, bad, ok in ((torch.float16, 2.0 ** -27, 2.0 ** -26), (torch.bfloat16, 2.0 ** -101, 2.0 ** -100)):
+        assert lib.rib_diff_attention_bwd(_attn(dtype=dtype, scale=bad), *ATTN_BWD) == UNSUPPORTED
+        assert lib.rib_diff_attention_bwd(_attn(dtype=dtype, scale=ok), *_with(ATTN_BWD, _0=None)) == INVALID   # the next check

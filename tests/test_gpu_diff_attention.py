@@ -472,3 +472,37 @@ def test_a_training_block(cuda_lib):
     got = _run(rib, a, d ** -0.5, t, window=window, width=W)
     val, tol = _reference(a, d ** -0.5, t, window=window, width=W)
     _compare(got, val, tol, t)
+
+
+@pytest.mark.parametrize("t", [F16, BF16])
+@pytest.mark.parametrize("d,dv", [(16, 32), (64, 128)])
+def test_small_scales(cuda_lib, d, dv, t):
+    """lse / scale far beyond fp16 (2^-8 of it is 2e5 here): large queries and keys under a scale of 2e-8."""
+    x = _inputs(1, 150, 190, 2, 1, d, dv, t)
+    for k in ("q1", "q2", "k1", "k2"):
+        x[k] *= 1500 * (64 / d) ** 0.25
+    x["do"] *= 256          # keeps the gradients of q and k among fp16's normal values
+    got = _run(cuda_lib, x, 2e-8, t)
+    val, tol = _reference(x, 2e-8, t)
+    _compare(got, val, tol, t, rms=ALL)
+
+
+def test_huge_scores(cuda_lib):
+    """Scores of millions: lse / scale is the raw score, above 2^24. Each row's own key outweighs all others."""
+    x = _inputs(1, 70, 70, 1, 1, 64, 128, F16)
+    for k in ("q1", "q2"):
+        x[k].copy_(torch.where(x[k] > 0, 600.0, -600.0))
+    for k in ("k1", "k2"):
+        x[k].copy_(x["q" + k[1]])
+    got = _run(cuda_lib, x, 0.125, F16)
+    # the own key scores 2.9e6 and the next 1e6 less: both maps are one-hot, o = (1 - lam) v. P is rounded (u) and so is o
+    lam, u, low = x["lam"].double(), torch.finfo(F16).eps / 2, 2.0 ** -24
+    v, do = x["v"].double().abs(), x["do"].double().abs()
+    assert ((got["o"].double() - (1 - lam) * x["v"].double()).abs() <= 3 * u * (1 + lam.abs()) * v + low).all()
+    # the log-sum-exp, 4.2e6 in powers of two, passes seven fp32 roundings of 2^-2 on its way into the backward's P: a factor
+    # of 2^1.75 at most. Nothing is lost beyond that: dv is P dO, and dP - D what the roundings of P, o and o2 leave
+    f = 2 ** 1.75 * (1 + 4 * u)
+    assert (got["dv"].double().abs() <= f * (1 + lam.abs()) * do + low).all()
+    e = f * (1 + lam.abs()) * 8 * u * (do * v).sum(-1).max()
+    for k in ("dq1", "dq2", "dk1", "dk2"):
+        assert (got[k].double().abs() <= 0.125 * 600 * e).all(), k

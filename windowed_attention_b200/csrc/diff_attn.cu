@@ -136,6 +136,10 @@ bool misaligned(std::initializer_list<const void*> ps, uintptr_t to) {
   return false;
 }
 
+// The backward's row constants hold lse / scale in three 16-bit terms; below
+// these scales the log-sum-exp of 2^31 equal keys alone leaves their range.
+float least_bwd_scale(const rib_diff_attn_desc* d) { return d->dtype == RIB_F16 ? 0x1p-26f : 0x1p-100f; }
+
 uintptr_t lam_size(const rib_diff_attn_desc* d) { return d->lam_dtype == RIB_F32 ? 4 : 2; }
 
 // Query boxes of one (sequence, key head) in the backward's row constants: whole tiles of two.
@@ -201,6 +205,7 @@ rib_status rib_diff_attention_bwd(const rib_diff_attn_desc* d, const void* q1, c
   rib_status st = geometry(who, d, &a.g);
   if (st != RIB_OK) return st;
   const DiffGeom& g = a.g;
+  if (d->scale < least_bwd_scale(d)) return bad(who, RIB_ERR_UNSUPPORTED, "scale below 2^-26 (fp16) or 2^-100 (bf16)");
   const bool rows = d->batch > 0 && d->q_len > 0, keys = d->batch > 0 && d->k_len > 0;
   if (!lam || !dlam || (rows && (!q1 || !q2 || !o || !o2 || !lse || !dO || !dq1 || !dq2)) ||
       (keys && (!k1 || !k2 || !v || !dk1 || !dk2 || !dv)))

@@ -261,14 +261,18 @@ struct DiffFwdArgs {
 // Row constants of the backward for every box of 64 query rows of every
 // (sequence, key head). First what the key-side kernel streams:
 //  * a [64][16] operand tile (32-byte rows, swizzled) whose columns hold
-//    c = -lse / scale of both maps and -D_1, each as three 16-bit terms that
-//    add up to 33 or 24 bits: 256 h + m + l. One more K step against a
-//    constant operand adds them to S_1, S_2 and dP inside the products.
+//    c = -lse / scale of both maps and -D_1, each as three 16-bit terms:
+//    2^15 h + 2^4 m + l. One more K step against a constant operand adds them to
+//    S_1, S_2 and dP inside the products. The factors are for fp16, whose h ends
+//    at 65504: |c| up to 2.1e9 is held, fp32's bits or 2^-25 of it (256 h + m + l
+//    ends at 1.7e7, which a row of eight keys passes at scale 1e-7). bf16 holds
+//    24 bits by any factors.
 //  * D_1 - D_2 and -lambda of each row.
 // Then what the query-side kernel reads once: -log2e lse1, -log2e lse2, -D_1,
 // -D_2, and where it leaves -sum_k P_2 dP for dlambda. Rows without a query
 // hold zeros: their Q and dO are zeros, and so is what they add.
 struct DiffRows {
+  static constexpr float kHigh = 32768.f, kMiddle = 16.f;   // factors of h and m
   static constexpr int kTile = 64 * 16 * 2;
   static constexpr int kDelta = kTile, kLam = kTile + 256, kStream = kTile + 512;   // bytes streamed
   static constexpr int kL1 = kStream, kL2 = kL1 + 256, kD1 = kL2 + 256, kD2 = kD1 + 256, kSum = kD2 + 256, kBytes = kSum + 256;

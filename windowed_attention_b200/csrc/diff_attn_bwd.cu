@@ -129,12 +129,12 @@ __global__ void __launch_bounds__(256) diff_attn_rows_kernel(const DiffBwdArgs a
   put(DiffRows::kD1, -d1);
   put(DiffRows::kD2, -d2);
   put(DiffRows::kSum, 0.f);
-  // x = 256 h + m + l in the operand type, each term the rounding of what is left
+  // x = 2^15 h + 2^4 m + r in the operand type, each term the rounding of what is left
   const auto terms = [](float x, float& h, float& m, float& r) {
-    h = diff_lo<F16>(diff_pack<F16>(x * (1.f / 256.f), 0.f));
-    const float y = fmaf(-256.f, h, x);
-    m = diff_lo<F16>(diff_pack<F16>(y, 0.f));
-    r = y - m;
+    h = diff_lo<F16>(diff_pack<F16>(x * (1.f / DiffRows::kHigh), 0.f));
+    const float y = fmaf(-DiffRows::kHigh, h, x);
+    m = diff_lo<F16>(diff_pack<F16>(y * (1.f / DiffRows::kMiddle), 0.f));
+    r = fmaf(-DiffRows::kMiddle, m, y);
   };
   const float inv = 1.f / g.scale_log2;
   float t[9];
@@ -579,9 +579,11 @@ diff_attn_dkv_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
     for (int i = Lay::OFF_ST + threadIdx.x * 16; i < Lay::OFF_X; i += kThreads * 16)
       *reinterpret_cast<uint4*>(smem + i) = make_uint4(0u, 0u, 0u, 0u);
   }
-  // three [128][16] operands, every row alike: 256, 1, 1 in the columns of S_1's, S_2's and dP's terms
+  // three [128][16] operands, every row alike: the terms' factors in the columns of S_1's, S_2's and dP's
   const auto constant = [](int which, int c) {
-    const auto at = [&](int i) { return i == 3 * which ? 256.f : (i == 3 * which + 1 || i == 3 * which + 2 ? 1.f : 0.f); };
+    const auto at = [&](int i) {
+      return i == 3 * which ? DiffRows::kHigh : (i == 3 * which + 1 ? DiffRows::kMiddle : (i == 3 * which + 2 ? 1.f : 0.f));
+    };
     return diff_pack<F16>(at(c), at(c + 1));
   };
   if (!Lay::A_TMEM)
