@@ -522,8 +522,10 @@ typedef struct {
  * with V. fp16 results saturate at +-65504. Few query rows over long keys run
  * as parts that a second kernel joins: workspace >=
  * rib_diff_attention_workspace_size() bytes (0 otherwise; NULL then). Tensors
- * and workspace 16-byte aligned. A row whose scores hold a NaN or an infinity
- * becomes NaN. Outputs may not overlap inputs. */
+ * and workspace 16-byte aligned. A row with a score of NaN or +infinity among the
+ * keys that it sees becomes NaN; a key that scores -infinity (a product beyond
+ * fp32 too) is one that the row does not see, here and in the backward. Outputs
+ * may not overlap inputs. */
 size_t rib_diff_attention_workspace_size(const rib_diff_attn_desc* desc);
 rib_status rib_diff_attention(const rib_diff_attn_desc* desc, const void* q1, const void* q2, const void* k1, const void* k2,
                               const void* v, const void* lam, const int* k_lens, void* o, void* o2, float* lse,

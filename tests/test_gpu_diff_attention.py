@@ -506,3 +506,41 @@ def test_huge_scores(cuda_lib):
     e = f * (1 + lam.abs()) * 8 * u * (do * v).sum(-1).max()
     for k in ("dq1", "dq2", "dk1", "dk2"):
         assert (got[k].double().abs() <= 0.125 * 600 * e).all(), k
+
+
+def test_infinite_scores(cuda_lib):
+    """Scores that overflow fp32: -infinity is a key that the row does not see, in both directions; +infinity spoils the row."""
+    t, N, r, h = BF16, 200, 3, 0
+    x = _inputs(1, N, N, 1, 1, 16, 32, t)
+    x["q1"][..., 0] = 0
+    x["k1"][..., 0] = -1e20
+    x["do"][0, r] = 0
+    want = _run(cuda_lib, x, 0.25, t)
+    g = torch.Generator().manual_seed(3)
+    x["do"][0, r] = torch.randn(1, 32, generator=g).to(t).cuda()
+    # every key of row r's first map scores -1e40: the map is empty, and has no part in any gradient
+    x["q1"][0, r, h, 0] = 1e20
+    got = _run(cuda_lib, x, 0.25, t)
+    others = torch.arange(N, device="cuda") != r
+    assert bool((got["lse"][0, 0, h, r] == -math.inf).all()) and torch.equal(got["lse"][1], want["lse"][1])
+    assert torch.equal(got["lse"][0][..., others], want["lse"][0][..., others])
+    for k in ("o", "o2", "dq1", "dq2"):
+        assert torch.equal(got[k][0, others], want[k][0, others]), k
+    u = torch.finfo(t).eps / 2
+    o, o2, lam = got["o"][0, r].double(), got["o2"][0, r].double(), x["lam"].double()
+    assert ((o + lam * o2).abs() <= 2 * u * (lam * o2).abs() + 1e-30).all()      # o and o2 are each rounded
+    assert bool((got["dq1"][0, r] == 0).all()) and torch.equal(got["dk1"], want["dk1"])
+    assert torch.isfinite(got["dk2"]).all() and torch.isfinite(got["dv"]).all() and bool((got["dq2"][0, r] != 0).any())
+    # some of them do: the row is the softmax over the rest
+    x["k1"][0, 100:, h, 0] = 0
+    got = _run(cuda_lib, x, 0.25, t)
+    a = [torch.softmax((x[q][0, r, h].double() @ x[k][0, at:, h].double().T * 0.25), -1) for q, k, at in (("q1", "k1", 100), ("q2", "k2", 0))]
+    v = x["v"][0, :, h].double()
+    ref, mag = a[0] @ v[100:] - lam * (a[1] @ v), a[0] @ v[100:].abs() + lam.abs() * (a[1] @ v.abs())
+    assert ((got["o"][0, r, h].double() - ref).abs() <= (u + 2.0 ** -16) * mag + u * ref.abs()).all()
+    for k in ("dq1", "dq2", "dk1", "dk2", "dv", "dlam"):
+        assert torch.isfinite(got[k]).all(), k
+    # and +infinity
+    x["q1"][0, 130, h, 0] = -1e20
+    o = _run(cuda_lib, x, 0.25, t, train=False)["o"]
+    assert torch.isnan(o[0, :, h]).all(1).nonzero()[:, 0].tolist() == [130] and int(torch.isnan(o).sum()) == 32

@@ -341,7 +341,7 @@ diff_attn_fwd_kernel(const __grid_constant__ CUtensorMap tm_q1, const __grid_con
             tmem_st8(tO + 8 * c, ov);
           }
         }
-        // rows that have seen nothing: reference 0; an infinite score has no softmax
+        // rows that have seen nothing (a score of -inf is a key not seen): reference 0; a score of +inf has no softmax
         const float ref = mx == -INFINITY ? 0.f : mx + (mx - mx);
         const uint64_t scale2 = f2_pack(sl2, sl2), ref2 = f2_pack(-ref, -ref);
         uint64_t sum0 = f2_pack(l * alpha, 0.f), sum1 = f2_pack(0.f, 0.f);
