@@ -503,7 +503,7 @@ typedef struct {
                                (<= 128), multiples of 8 */
   rib_dtype dtype;          /* of every tensor but lam: RIB_BF16 or RIB_F16 */
   rib_dtype lam_dtype;      /* of lam and dlam: RIB_F32 or dtype */
-  float scale;              /* > 0 */
+  float scale;              /* > 0, below 2.3e38 (scale log2 e is finite) */
   int causal;               /* query t sees the keys up to t + keys - q_len */
   int window, width;        /* both 0: sequences; window <= 1024 */
   /* elements between batch items, tokens and heads; three zeros: contiguous.

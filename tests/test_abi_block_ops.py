@@ -220,3 +220,10 @@ def test_diff_attention_backward_scale_range(lib):
     for dtype, bad, ok in ((torch.float16, 2.0 ** -27, 2.0 ** -26), (torch.bfloat16, 2.0 ** -101, 2.0 ** -100)):
         assert lib.rib_diff_attention_bwd(_attn(dtype=dtype, scale=bad), *ATTN_BWD) == UNSUPPORTED
         assert lib.rib_diff_attention_bwd(_attn(dtype=dtype, scale=ok), *_with(ATTN_BWD, _0=None)) == INVALID   # the next check
+
+
+def test_diff_attention_scale_in_powers_of_two(lib):
+    # a finite scale whose product with log2 e is not
+    for scale, st in ((2.4e38, INVALID), (2.3e38, 0)):
+        d = _attn(scale=scale, batch=0)
+        assert lib.rib_diff_attention(d, *ATTN) == st

@@ -86,7 +86,8 @@ rib_status geometry(const char* who, const rib_diff_attn_desc* d, DiffGeom* g) {
   if (d->batch < 0 || d->q_len < 0 || d->k_len < 0 || d->q_heads <= 0 || d->kv_heads <= 0 || d->d <= 0 || d->dv <= 0)
     return bad(who, RIB_ERR_INVALID_ARG, "sizes: batch and lengths >= 0, heads and widths positive");
   if (d->q_heads % d->kv_heads) return bad(who, RIB_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
-  if (!(d->scale > 0.f) || !std::isfinite(d->scale)) return bad(who, RIB_ERR_INVALID_ARG, "scale must be positive and finite");
+  // the kernels' exponents are powers of two
+  if (!(d->scale > 0.f) || !std::isfinite(d->scale * kDiffLog2e)) return bad(who, RIB_ERR_INVALID_ARG, "scale must be positive and below 2.3e38");
   if (d->dtype != RIB_BF16 && d->dtype != RIB_F16) return bad(who, RIB_ERR_INVALID_ARG, "dtype must be RIB_BF16 or RIB_F16");
   if (d->lam_dtype != RIB_F32 && d->lam_dtype != d->dtype)
     return bad(who, RIB_ERR_INVALID_ARG, "lam_dtype must be RIB_F32 or dtype");
