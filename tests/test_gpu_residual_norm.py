@@ -354,3 +354,34 @@ def test_dropped_elements_have_no_gradient(cuda_lib, C, post):
             assert torch.isfinite(v).all(), k
             assert torch.equal(v, got[k]), f"{k}: {int((v != got[k]).sum())} of {v.numel()} differ"
     _check(cuda_lib, T, C, F32, BF16, "layer", post, True, T, p, rpg=1)
+
+
+@pytest.mark.parametrize("groups", [1, 3])
+def test_weights_of_a_flat_buffer(cuda_lib, groups):
+    """Weights are read one element at a time: slices of a parameter buffer that start off a 16-byte boundary give the bits of
+    aligned ones (the same vectors and the same order of sums), and their gradients go into such slices."""
+    rib, T, C, p = cuda_lib, 51, 180, 0.1
+    a = _make(T, C, F32, BF16, "layer", "layer", True, groups)
+    rpg = T // groups
+    want = _run(rib, a, T, C, F32, BF16, "layer", "layer", rpg, p)
+    names = ORDER[1:]
+    at, n = {}, 1
+    for k in names:
+        at[k] = (n, n + a[k].numel())
+        n += a[k].numel() + 1
+    flat, grads = (torch.full((n,), float("nan"), device="cuda") for _ in range(2))
+    w, dw = ({k: b[at[k][0]:at[k][1]].view(a[k].shape) for k in names} for b in (flat, grads))
+    d = {k: v.cuda() for k, v in a.items()}
+    for k in names:
+        w[k].copy_(a[k])
+    assert any(w[k].data_ptr() % 16 for k in names)
+    desc = rib.residual_norm_desc(T, C, F32, BF16, pre="layer", post="layer", eps=EPS, rows_per_group=rpg, p=p, seed=11, offset=5)
+    x_out, h, dx, dy, dgate = (torch.empty_like(d[k]) for k in ("x", "y", "x", "y", "gate"))
+    rib.rib_residual_norm(desc, d["x"], d["y"], d["gate"], *(w[k] for k in names), x_out, h)
+    ws = torch.empty(rib.rib_residual_norm_bwd_workspace_size(desc), dtype=torch.uint8, device="cuda")
+    rib.rib_residual_norm_bwd(desc, x_out, d["y"], d["gate"], *(w[k] for k in names[:4]), d["dx_out"], d["dh"], dx, dy, dgate,
+                              *(dw[k] for k in names), ws)
+    got = {"x_out": x_out, "h": h, "dx": dx, "dy": dy, "dgate": dgate, **{"d" + k: dw[k] for k in names}}
+    for k, v in got.items():
+        assert torch.equal(v, want[k]), k
+    assert int(torch.isnan(grads).sum()) == n - sum(a[k].numel() for k in names)     # nothing between the slices

@@ -905,7 +905,7 @@ int group_count(const rib_residual_norm_desc* d) {
   return d->T > 0 ? static_cast<int>((d->T - 1) / d->rows_per_group + 1) : 1;
 }
 
-// Vectors of four need C % 4 == 0 and every tensor on a vector's boundary.
+// Vectors of four need C % 4 == 0 and the tensors that move in blocks on a vector's boundary (weights are read by element).
 struct Aligner {
   bool vec = true, element = true, bulk = true;   // bulk: 16 bytes
   void add(const void* p, int dtype) {
@@ -938,13 +938,13 @@ rib_status rib_residual_norm(const rib_residual_norm_desc* d, const void* x, con
   if (y && !x_out && !h) return bad(who, RIB_ERR_INVALID_ARG, "nothing to write: neither x_out nor h");
   if ((post_w || post_b) && d->post == RIB_NORM_NONE) return bad(who, RIB_ERR_INVALID_ARG, "post_w and post_b need a post norm");
   if ((pre_w || pre_b) && d->pre == RIB_NORM_NONE) return bad(who, RIB_ERR_INVALID_ARG, "pre_w and pre_b need a pre norm");
-  Aligner a;
+  Aligner a;   // the tensors that move in blocks
   a.add(x, d->x_dtype);
   a.add(x_out, d->x_dtype);
   for (const void* q : {y, gate, static_cast<const void*>(h)}) a.add(q, d->dtype);
-  const Aligner t = a;   // the tensors that move in blocks
-  for (const float* q : {scale, post_w, post_b, pre_w, pre_b}) a.add(q, RIB_F32);
-  if (!a.element || reinterpret_cast<uintptr_t>(step) % 8) return bad(who, RIB_ERR_ALIGNMENT, "tensors need their element's alignment, step 8 bytes");
+  Aligner b;   // read one element at a time
+  for (const float* q : {scale, post_w, post_b, pre_w, pre_b}) b.add(q, RIB_F32);
+  if (!a.element || !b.element || reinterpret_cast<uintptr_t>(step) % 8) return bad(who, RIB_ERR_ALIGNMENT, "tensors need their element's alignment, step 8 bytes");
   NormParams p{};
   p.T = d->T; p.C = d->C; p.rows_per_group = d->rows_per_group; p.pre = d->pre; p.post = d->post;
   p.eps = d->eps; p.inv_c = 1.f / d->C;
@@ -954,11 +954,11 @@ rib_status rib_residual_norm(const rib_residual_norm_desc* d, const void* x, con
   make_drop_rng(d->p, d->seed, d->offset, step, &p.rng);
   const bool vec = a.vec && d->C % 4 == 0;
   cudaError_t e;
-  if (d->x_dtype == RIB_BF16) e = launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, stream);
-  else if (d->x_dtype == RIB_F16) e = launch_fwd<__half, __half>(p, vec, t.bulk, stream);
-  else if (d->dtype == RIB_BF16) e = launch_fwd<float, __nv_bfloat16>(p, vec, t.bulk, stream);
-  else if (d->dtype == RIB_F16) e = launch_fwd<float, __half>(p, vec, t.bulk, stream);
-  else e = launch_fwd<float, float>(p, vec, t.bulk, stream);
+  if (d->x_dtype == RIB_BF16) e = launch_fwd<__nv_bfloat16, __nv_bfloat16>(p, vec, a.bulk, stream);
+  else if (d->x_dtype == RIB_F16) e = launch_fwd<__half, __half>(p, vec, a.bulk, stream);
+  else if (d->dtype == RIB_BF16) e = launch_fwd<float, __nv_bfloat16>(p, vec, a.bulk, stream);
+  else if (d->dtype == RIB_F16) e = launch_fwd<float, __half>(p, vec, a.bulk, stream);
+  else e = launch_fwd<float, float>(p, vec, a.bulk, stream);
   if (e != cudaSuccess) return cuda_fail(e, "rib_residual_norm launch");
   return RIB_OK;
 }
@@ -992,14 +992,13 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_
   const bool sums = dscale || dpost_w || dpost_b || dpre_w || dpre_b;
   if (sums && rows && !ws) return bad(who, RIB_ERR_INVALID_ARG, "weight gradients need the workspace");
   if (sums && ws_bytes < rib_residual_norm_bwd_workspace_size(d)) return bad(who, RIB_ERR_INVALID_ARG, "workspace too small");
-  Aligner a;
+  Aligner a;   // the tensors that move in blocks
   a.add(x_out, d->x_dtype);
   a.add(dx_out, d->x_dtype);
   a.add(dx, d->x_dtype);
   for (const void* q : {y, gate, dh, static_cast<const void*>(dy), static_cast<const void*>(dgate)}) a.add(q, d->dtype);
-  const Aligner t = a;   // the tensors that move in blocks
-  for (const float* q : {scale, post_w, post_b, pre_w}) a.add(q, RIB_F32);
-  Aligner b;   // written one element at a time
+  Aligner b;   // read or written one element at a time
+  for (const float* q : {scale, post_w, post_b, pre_w}) b.add(q, RIB_F32);
   for (const float* q : {dscale, dpost_w, dpost_b, dpre_w, dpre_b}) b.add(q, RIB_F32);
   b.add(ws, RIB_F32);
   if (!a.element || !b.element || reinterpret_cast<uintptr_t>(step) % 8)
@@ -1018,11 +1017,11 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* d, const void* x_
     if (!(p.err = device_error_word())) return bad(who, RIB_ERR_CUDA, "no device error word");
     make_drop_rng(d->p, d->seed, d->offset, step, &p.rng);
     const bool vec = a.vec && d->C % 4 == 0;
-    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, t.bulk, groups, &sp.chunks, stream);
-    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, t.bulk, groups, &sp.chunks, stream);
-    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, t.bulk, groups, &sp.chunks, stream);
-    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, t.bulk, groups, &sp.chunks, stream);
-    else e = launch_bwd<float, float>(p, vec, t.bulk, groups, &sp.chunks, stream);
+    if (d->x_dtype == RIB_BF16) e = launch_bwd<__nv_bfloat16, __nv_bfloat16>(p, vec, a.bulk, groups, &sp.chunks, stream);
+    else if (d->x_dtype == RIB_F16) e = launch_bwd<__half, __half>(p, vec, a.bulk, groups, &sp.chunks, stream);
+    else if (d->dtype == RIB_BF16) e = launch_bwd<float, __nv_bfloat16>(p, vec, a.bulk, groups, &sp.chunks, stream);
+    else if (d->dtype == RIB_F16) e = launch_bwd<float, __half>(p, vec, a.bulk, groups, &sp.chunks, stream);
+    else e = launch_bwd<float, float>(p, vec, a.bulk, groups, &sp.chunks, stream);
     if (e != cudaSuccess) return cuda_fail(e, "rib_residual_norm_bwd launch");
   }
   if (!sums) return RIB_OK;
