@@ -227,3 +227,13 @@ def test_diff_attention_scale_in_powers_of_two(lib):
     for scale, st in ((2.4e38, INVALID), (2.3e38, 0)):
         d = _attn(scale=scale, batch=0)
         assert lib.rib_diff_attention(d, *ATTN) == st
+
+
+def test_a_descriptor_made_field_by_field(monkeypatch):
+    # the first call of a process, with a descriptor that no helper made: its tensors have the descriptor's type
+    monkeypatch.setattr(_lib, "_TORCH_CODE", {})
+    t = torch.zeros(1, 4, 2, 16, dtype=torch.bfloat16)
+    assert _lib._strided_arg("q1", t, (1, 4, 2, 16), None, _lib.RIB_BF16, t.get_device()) == t.data_ptr()
+    monkeypatch.setattr(_lib, "_TORCH_CODE", {})
+    with pytest.raises(ValueError):
+        _lib._strided_arg("q1", t, (1, 4, 2, 16), None, _lib.RIB_F16, t.get_device())

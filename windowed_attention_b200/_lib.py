@@ -394,16 +394,20 @@ def rib_conv_ffn(xn, x, B, H, W, C, hidden, W1, b1, Wf, bf, W2, b2, workspace, s
 # These calls check what the C interface cannot see: that every tensor is on
 # the current device (the kernels run there), has its type and holds enough.
 _NORMS = {"none": 0, "layer": 1, "rms": 2}
-_TORCH_CODE = {}
+_TORCH_CODE = {}   # filled when the first of these calls needs torch
+
+
+def _codes() -> dict:
+    if not _TORCH_CODE:
+        import torch
+        _TORCH_CODE.update({torch.bfloat16: RIB_BF16, torch.float32: RIB_F32, torch.float16: RIB_F16})
+    return _TORCH_CODE
 
 
 def _code(dtype) -> int:
     """RIB_* code of a torch dtype; anything but bf16, fp32 and fp16 is refused."""
-    if not _TORCH_CODE:
-        import torch
-        _TORCH_CODE.update({torch.bfloat16: RIB_BF16, torch.float32: RIB_F32, torch.float16: RIB_F16})
     try:
-        return _TORCH_CODE[dtype]
+        return (_TORCH_CODE or _codes())[dtype]
     except KeyError:
         raise ValueError(f"dtype {dtype}: librib takes bfloat16, float32 and float16") from None
 
@@ -529,7 +533,7 @@ def _strided_arg(name, t, shape, strides, desc_code, device) -> Optional[int]:
         return None
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
-    if _TORCH_CODE.get(t.dtype) != desc_code:
+    if (_TORCH_CODE or _codes()).get(t.dtype) != desc_code:
         raise ValueError(f"{name} is {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} is {tuple(t.shape)}, the descriptor says {shape}")
