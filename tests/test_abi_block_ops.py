@@ -237,3 +237,19 @@ def test_a_descriptor_made_field_by_field(monkeypatch):
     monkeypatch.setattr(_lib, "_TORCH_CODE", {})
     with pytest.raises(ValueError):
         _lib._strided_arg("q1", t, (1, 4, 2, 16), None, _lib.RIB_F16, t.get_device())
+
+
+def test_row_shapes_of_the_binding():
+    f = lambda shape, want, t=torch.float32: _lib._row_arg("x", torch.zeros(shape, dtype=t), want, _lib.RIB_F32, -1)  # noqa: E731
+    for shape in ((6, 40), (240,), (2, 3, 40), (6, 1, 40)):
+        assert f(shape, (6, 40))
+    assert f((40,), (40,)) and f((1, 40), (40,)) and f((0, 40), (0, 40)) is not None
+    for shape, want in (((40, 6), (6, 40)), ((7, 40), (6, 40)), ((5, 40), (6, 40)), ((241,), (6, 40)), ((41,), (40,)), ((40, 1), (40,)),
+                        ((2, 40), (40,)), ((), (6, 40))):
+        with pytest.raises(ValueError):
+            f(shape, want)
+    with pytest.raises(ValueError):
+        f((6, 40), (6, 40), torch.bfloat16)
+    with pytest.raises(ValueError):
+        _lib._row_arg("x", torch.zeros(40, 6).t(), (6, 40), _lib.RIB_F32, -1)
+    assert _lib._row_arg("x", None, (6, 40), _lib.RIB_F32, -1) is None

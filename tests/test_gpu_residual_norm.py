@@ -385,3 +385,36 @@ def test_weights_of_a_flat_buffer(cuda_lib, groups):
     for k, v in got.items():
         assert torch.equal(v, want[k]), k
     assert int(torch.isnan(grads).sum()) == n - sum(a[k].numel() for k in names)     # nothing between the slices
+
+
+def test_tensors_of_other_shapes_are_refused(cuda_lib):
+    """Tensors hold the descriptor's rows of C values: flat or any shape that ends in C, no more and no fewer."""
+    rib, T, C = cuda_lib, 6, 40
+    f = lambda *s, t=F32: torch.randn(*s, device="cuda").to(t)  # noqa: E731
+    desc = rib.residual_norm_desc(T, C, F32, BF16, pre="layer", post="layer", rows_per_group=3)
+    ok = {"x": f(T, C), "y": f(T, C, t=BF16), "gate": f(T, C, t=BF16), "scale": f(2, C), "post_w": f(C), "post_b": f(C), "pre_w": f(C),
+          "pre_b": f(C), "x_out": f(T, C), "h": f(T, C, t=BF16)}
+    rib.rib_residual_norm(desc, **ok)
+    for k, v in ok.items():
+        for bad in (f(2 * v.numel() // C, C), f(C, v.numel() // C), f(v.numel() - C), f(v.numel() + C)):
+            with pytest.raises(ValueError, match=k):
+                rib.rib_residual_norm(desc, **{**ok, k: bad.to(v.dtype)})
+    for shape in ((T * C,), (2, 3, C), (1, T, 1, C)):
+        out = {k: torch.empty(shape, device="cuda", dtype=ok[k].dtype) for k in ("x_out", "h")}
+        rib.rib_residual_norm(desc, **{**ok, **{k: ok[k].view(shape) for k in ("x", "y", "gate")}, **out})
+        assert all(torch.equal(out[k].view(T, C), ok[k]) for k in out)
+    grads = {"d" + k: torch.empty_like(ok[k]) for k in ("x", "y", "gate", "scale", "post_w", "post_b", "pre_w", "pre_b")}
+    args = {k: ok[k] for k in ("x_out", "y", "gate", "scale", "post_w", "post_b", "pre_w")}
+    args.update(grads, dx_out=f(T, C), dh=f(T, C, t=BF16),
+                workspace=torch.empty(rib.rib_residual_norm_bwd_workspace_size(desc), dtype=torch.uint8, device="cuda"))
+    rib.rib_residual_norm_bwd(desc, **args)
+    for k, v in args.items():
+        if k != "workspace":
+            with pytest.raises(ValueError, match=k):
+                rib.rib_residual_norm_bwd(desc, **{**args, k: torch.empty(C, v.numel() // C, device="cuda", dtype=v.dtype)})
+    # no rows: a scale of any number of rows
+    none = rib.residual_norm_desc(0, C, F32, BF16, pre="layer")
+    e = lambda t: torch.empty(0, C, dtype=t, device="cuda")  # noqa: E731
+    rib.rib_residual_norm(none, e(F32), e(BF16), scale=f(1, C), x_out=e(F32), h=e(BF16))
+    rib.rib_residual_norm_bwd(none, e(F32), e(BF16), scale=f(1, C), dx_out=e(F32), dh=e(BF16), dscale=f(1, C), dx=e(F32), dy=e(BF16))
+    rib.rib_residual_norm_bwd(none, e(F32), e(BF16), dx_out=e(F32), dh=e(BF16), dscale=f(1, C), dx=e(F32), dy=e(BF16))

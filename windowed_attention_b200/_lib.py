@@ -161,15 +161,16 @@ def _ptr(t) -> Optional[int]:
 _raw_stream = None
 
 
-def _stream(stream) -> Optional[int]:
+def _stream(stream, device=None) -> Optional[int]:
+    """Handle of `stream`, by default the current one of `device` (by default the current device)."""
     if stream is None:
         global _raw_stream
         if _raw_stream is None:
             import torch
             # the stream's handle without a Stream object around it, where torch offers that
             get, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), torch.cuda.current_device
-            _raw_stream = (lambda: get(dev())) if get else (lambda: torch.cuda.current_stream().cuda_stream)
-        return _raw_stream()
+            _raw_stream = (lambda d: get(dev() if d is None else d)) if get else (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        return _raw_stream(device)
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
@@ -412,13 +413,19 @@ def _code(dtype) -> int:
         raise ValueError(f"dtype {dtype}: librib takes bfloat16, float32 and float16") from None
 
 
+_device_now = None
+
+
 def _current_device(t) -> int:
-    import torch
+    global _device_now
+    if _device_now is None:
+        import torch
+        _device_now = torch.cuda.current_device
     at = t.get_device()
     if at < 0:
         raise ValueError("librib entry points take device tensors")
-    if at != torch.cuda.current_device():
-        raise ValueError(f"tensor on {t.device} while the current device is cuda:{torch.cuda.current_device()}: "
+    if at != _device_now():
+        raise ValueError(f"tensor on {t.device} while the current device is cuda:{_device_now()}: "
                          "make its device current for the call")
     return at
 
@@ -433,6 +440,26 @@ def _arg(name, t, numel, code, device) -> Optional[int]:
         raise ValueError(f"{name} is {t.dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} holds {t.numel()} values, {numel} are needed")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: librib entry points take contiguous tensors")
+    return t.data_ptr()
+
+
+def _rows_of(t, want) -> bool:
+    """True where `t` holds the values of a tensor of shape `want`, (rows, C) or (C,), by another shape: flat, or one that ends in C."""
+    return t.numel() == want[0] * (want[1] if len(want) > 1 else 1) and (t.dim() == 1 or t.shape[-1:] == want[-1:])
+
+
+def _row_arg(name, t, want, code, device) -> Optional[int]:
+    """Pointer of a contiguous device tensor of type `code` that holds `want`, (rows, C) or (C,), values."""
+    if t is None:
+        return None
+    if t.shape != want and not _rows_of(t, want):
+        raise ValueError(f"{name} is {tuple(t.shape)}, the descriptor says {want}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}: librib entry points take tensors of the current device, cuda:{device}")
+    if (_TORCH_CODE or _codes()).get(t.dtype) != code:
+        raise ValueError(f"{name} is {t.dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: librib entry points take contiguous tensors")
     return t.data_ptr()
@@ -458,7 +485,7 @@ def rib_dropout(x, y, p, seed, offset=0, step=None, stream=None) -> None:
     if y.numel() != n:
         raise ValueError(f"y holds {y.numel()} values, x {n}")
     _check(_lib.rib_dropout(_arg("x", x, n, code, dev), _arg("y", y, n, code, dev), code, n, float(p), int(seed),
-                            int(offset), _step_arg(step, dev), _stream(stream)))
+                            int(offset), _step_arg(step, dev), _stream(stream, dev)))
 
 
 def residual_norm_desc(T, C, x_dtype, dtype, pre="layer", post="none", eps=1e-5, rows_per_group=None, p=0.0, seed=0,
@@ -474,22 +501,27 @@ def residual_norm_desc(T, C, x_dtype, dtype, pre="layer", post="none", eps=1e-5,
                             _NORMS[pre], _NORMS[post], float(eps), float(p), int(seed), int(offset))
 
 
-def _norm_groups(d: ResidualNormDesc) -> int:
-    return -(-d.T // d.rows_per_group) if d.rows_per_group > 0 else 0
+def _scale_shape(d: ResidualNormDesc, scale) -> tuple:
+    """Rows and width of scale and its gradient; without rows of x any number of rows."""
+    if d.T > 0 and d.rows_per_group > 0:
+        return (-(-d.T // d.rows_per_group), d.C)
+    return (0 if scale is None else scale.numel() // max(1, d.C), d.C)
 
 
 def rib_residual_norm(desc: ResidualNormDesc, x, y=None, gate=None, scale=None, post_w=None, post_b=None, pre_w=None,
                       pre_b=None, x_out=None, h=None, step=None, stream=None) -> None:
     """x_out = x + dropout(scale * gate * (N_post(y) post_w + post_b)) and
-    h = N_pre(x_out) pre_w + pre_b (see include/rib.h)."""
+    h = N_pre(x_out) pre_w + pre_b (see include/rib.h). Tensors hold the
+    descriptor's rows of C values, in any shape that ends in C or flat."""
     load()
-    dev, d = _current_device(x), desc
-    n, C, xc, c = d.T * d.C, d.C, d.x_dtype, d.dtype
+    dev, d, arg = _current_device(x), desc, _row_arg
+    C, xc, c = d.C, d.x_dtype, d.dtype
+    n, w = (d.T, C), (C,)
     _check(_lib.rib_residual_norm(
-        ctypes.byref(d), _arg("x", x, n, xc, dev), _arg("y", y, n, c, dev), _arg("gate", gate, n, c, dev),
-        _arg("scale", scale, _norm_groups(d) * C, RIB_F32, dev), _arg("post_w", post_w, C, RIB_F32, dev),
-        _arg("post_b", post_b, C, RIB_F32, dev), _arg("pre_w", pre_w, C, RIB_F32, dev), _arg("pre_b", pre_b, C, RIB_F32, dev),
-        _arg("x_out", x_out, n, xc, dev), _arg("h", h, n, c, dev), _step_arg(step, dev), _stream(stream)))
+        ctypes.byref(d), arg("x", x, n, xc, dev), arg("y", y, n, c, dev), arg("gate", gate, n, c, dev),
+        arg("scale", scale, _scale_shape(d, scale), RIB_F32, dev), arg("post_w", post_w, w, RIB_F32, dev), arg("post_b", post_b, w, RIB_F32, dev),
+        arg("pre_w", pre_w, w, RIB_F32, dev), arg("pre_b", pre_b, w, RIB_F32, dev), arg("x_out", x_out, n, xc, dev), arg("h", h, n, c, dev),
+        _step_arg(step, dev), _stream(stream, dev)))
 
 
 def rib_residual_norm_bwd_workspace_size(desc: ResidualNormDesc) -> int:
@@ -502,17 +534,17 @@ def rib_residual_norm_bwd(desc: ResidualNormDesc, x_out, y=None, gate=None, scal
     """Gradients of rib_residual_norm from dx_out (the stream's, may be None)
     and dh; each output may be None (see include/rib.h)."""
     load()
-    d = desc
+    d, arg = desc, _row_arg
     dev = _current_device(x_out if x_out is not None else dx_out)
-    n, C, xc, c, g = d.T * d.C, d.C, d.x_dtype, d.dtype, _norm_groups(d) * d.C
+    C, xc, c = d.C, d.x_dtype, d.dtype
+    n, w, g = (d.T, C), (C,), _scale_shape(d, dscale if scale is None else scale)
     _check(_lib.rib_residual_norm_bwd(
-        ctypes.byref(d), _arg("x_out", x_out, n, xc, dev), _arg("y", y, n, c, dev), _arg("gate", gate, n, c, dev),
-        _arg("scale", scale, g, RIB_F32, dev), _arg("post_w", post_w, C, RIB_F32, dev), _arg("post_b", post_b, C, RIB_F32, dev),
-        _arg("pre_w", pre_w, C, RIB_F32, dev), _arg("dx_out", dx_out, n, xc, dev), _arg("dh", dh, n, c, dev),
-        _arg("dx", dx, n, xc, dev), _arg("dy", dy, n, c, dev), _arg("dgate", dgate, n, c, dev),
-        _arg("dscale", dscale, g, RIB_F32, dev), _arg("dpost_w", dpost_w, C, RIB_F32, dev),
-        _arg("dpost_b", dpost_b, C, RIB_F32, dev), _arg("dpre_w", dpre_w, C, RIB_F32, dev),
-        _arg("dpre_b", dpre_b, C, RIB_F32, dev), *_workspace_arg(workspace, dev), _step_arg(step, dev), _stream(stream)))
+        ctypes.byref(d), arg("x_out", x_out, n, xc, dev), arg("y", y, n, c, dev), arg("gate", gate, n, c, dev),
+        arg("scale", scale, g, RIB_F32, dev), arg("post_w", post_w, w, RIB_F32, dev), arg("post_b", post_b, w, RIB_F32, dev),
+        arg("pre_w", pre_w, w, RIB_F32, dev), arg("dx_out", dx_out, n, xc, dev), arg("dh", dh, n, c, dev), arg("dx", dx, n, xc, dev),
+        arg("dy", dy, n, c, dev), arg("dgate", dgate, n, c, dev), arg("dscale", dscale, g, RIB_F32, dev),
+        arg("dpost_w", dpost_w, w, RIB_F32, dev), arg("dpost_b", dpost_b, w, RIB_F32, dev), arg("dpre_w", dpre_w, w, RIB_F32, dev),
+        arg("dpre_b", dpre_b, w, RIB_F32, dev), *_workspace_arg(workspace, dev), _step_arg(step, dev), _stream(stream, dev)))
 
 
 def diff_attn_desc(batch, q_len, k_len, q_heads, kv_heads, d, dv, scale, dtype, lam_dtype=None, causal=False, window=0, width=0,
@@ -593,7 +625,7 @@ def rib_diff_attention(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens=None, 
         ctypes.byref(desc), arg("q1", q1, qs, qt, code, dev), arg("q2", q2, qs, qt, code, dev), arg("k1", k1, ks, kt, code, dev),
         arg("k2", k2, ks, kt, code, dev), arg("v", v, vs, vt, code, dev), _arg("lam", lam, heads, lam_code, dev),
         _lens_arg(k_lens, batch, dev), arg("o", o, os, ot, code, dev), arg("o2", o2, os, ot, code, dev), _arg("lse", lse, rows, RIB_F32, dev),
-        *_workspace_arg(workspace, dev), _stream(stream)))
+        *_workspace_arg(workspace, dev), _stream(stream, dev)))
 
 
 def rib_diff_attention_bwd_workspace_size(desc: DiffAttnDesc) -> int:
@@ -614,4 +646,4 @@ def rib_diff_attention_bwd(desc: DiffAttnDesc, q1, q2, k1, k2, v, lam, k_lens, o
         _lens_arg(k_lens, batch, dev), arg("o", o, os, ot, code, dev), arg("o2", o2, os, ot, code, dev), _arg("lse", lse, rows, RIB_F32, dev),
         arg("do", do, os, ot, code, dev), arg("dq1", dq1, qs, qt, code, dev), arg("dq2", dq2, qs, qt, code, dev),
         arg("dk1", dk1, ks, kt, code, dev), arg("dk2", dk2, ks, kt, code, dev), arg("dv", dv, vs, vt, code, dev),
-        _arg("dlam", dlam, heads, lam_code, dev), *_workspace_arg(workspace, dev), _stream(stream)))
+        _arg("dlam", dlam, heads, lam_code, dev), *_workspace_arg(workspace, dev), _stream(stream, dev)))
