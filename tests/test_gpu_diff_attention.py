@@ -544,3 +544,28 @@ def test_infinite_scores(cuda_lib):
     x["q1"][0, 130, h, 0] = -1e20
     o = _run(cuda_lib, x, 0.25, t, train=False)["o"]
     assert torch.isnan(o[0, :, h]).all(1).nonzero()[:, 0].tolist() == [130] and int(torch.isnan(o).sum()) == 32
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("d,dv", [(64, 128), (48, 104), (64, 64), (24, 40)])
+@pytest.mark.parametrize("H,W,window,Hq,Hk", [(13, 29, 8, 2, 2), (40, 33, 31, 2, 1), (20, 70, 64, 4, 2), (9, 7, 16, 3, 1)])
+def test_windows_of_every_width_class(cuda_lib, H, W, window, Hq, Hk, d, dv, t):
+    """Cut boxes and shared heads with one score buffer in the key-side kernel (dv above 64) and with two."""
+    _check(cuda_lib, 2, H * W, H * W, Hq, Hk, d, dv, t, window=window, width=W)
+
+
+@pytest.mark.parametrize("d,dv", [(64, 128), (32, 64)])
+def test_a_bad_window_stays_in_its_window_at_wide_heads(cuda_lib, d, dv):
+    t, H, W, window = BF16, 26, 29, 12
+    x = _inputs(1, H * W, H * W, 2, 1, d, dv, t)
+    one = _run(cuda_lib, x, 0.125, t, window=window, width=W)
+    bad = torch.zeros(H, W, dtype=torch.bool, device="cuda")
+    bad[window:2 * window, :window] = True
+    bad = bad.reshape(-1)
+    for k in NAMES + ("do",):
+        x[k][0, bad] = float("nan")
+    two = _run(cuda_lib, x, 0.125, t, window=window, width=W)
+    for k in ("o", "o2", "dq1", "dq2", "dk1", "dk2", "dv"):
+        assert torch.equal(one[k][0, ~bad], two[k][0, ~bad]), k
+        assert torch.isnan(two[k][0, bad]).all(), k
+    assert torch.equal(one["lse"][..., ~bad], two["lse"][..., ~bad])

@@ -418,3 +418,46 @@ def test_tensors_of_other_shapes_are_refused(cuda_lib):
     rib.rib_residual_norm(none, e(F32), e(BF16), scale=f(1, C), x_out=e(F32), h=e(BF16))
     rib.rib_residual_norm_bwd(none, e(F32), e(BF16), scale=f(1, C), dx_out=e(F32), dh=e(BF16), dscale=f(1, C), dx=e(F32), dy=e(BF16))
     rib.rib_residual_norm_bwd(none, e(F32), e(BF16), dx_out=e(F32), dh=e(BF16), dscale=f(1, C), dx=e(F32), dy=e(BF16))
+
+
+@pytest.mark.parametrize("T,rpg,C", [(50, 17, 37), (9, 1, 51), (31, 5, 1021), (8, 3, 2047), (60, 7, 3), (45, 11, 46)])
+@pytest.mark.parametrize("p", [0.0, 0.2])
+def test_row_groups_at_odd_widths(cuda_lib, T, rpg, C, p):
+    """Groups that start on odd rows, whose rows of an odd width start one element early in pairs."""
+    _check(cuda_lib, T, C, F32, BF16, "rms", "layer", True, -(-T // rpg), p, rpg=rpg)
+
+
+@pytest.mark.parametrize("C", [8, 37, 180, 1021])
+@pytest.mark.parametrize("xt,t", [(F32, BF16), (F16, F16)])
+def test_tensors_off_a_16_byte_boundary(cuda_lib, C, xt, t, monkeypatch):
+    """Every [T, C] tensor starts one element into its buffer, forward and backward: the oracle's values, and nothing around
+    the tensors is written."""
+    rib, buffers = cuda_lib, []
+
+    def shifted(v):
+        if v is None or v.dim() != 2 or v.shape[0] != T:
+            return v
+        buf = torch.full((v.numel() + 9,), 7.0, dtype=v.dtype, device="cuda")
+        w = buf[1:1 + v.numel()].view(v.shape)
+        w.copy_(v)
+        buffers.append((buf, v.numel()))
+        return w
+
+    T = 37
+    run = {n: getattr(rib, n) for n in ("rib_residual_norm", "rib_residual_norm_bwd")}
+
+    def through(name):
+        def call(desc, *args, step=None):
+            own = [shifted(a) if torch.is_tensor(a) else a for a in args]
+            run[name](desc, *own, step=step)
+            for a, b in zip(args, own):
+                if a is not b:
+                    a.copy_(b)
+        return call
+
+    for n in run:
+        monkeypatch.setattr(rib, n, through(n))
+    _check(rib, T, C, xt, t, "layer", "layer", True, 1, 0.2)
+    assert len(buffers) == 5 + 8      # x, y, gate, x_out, h; x_out, y, gate, dx_out, dh, dx, dy, dgate
+    for buf, n in buffers:
+        assert buf[0] == 7 and bool((buf[1 + n:] == 7).all())
