@@ -253,3 +253,16 @@ def test_row_shapes_of_the_binding():
     with pytest.raises(ValueError):
         _lib._row_arg("x", torch.zeros(40, 6).t(), (6, 40), _lib.RIB_F32, -1)
     assert _lib._row_arg("x", None, (6, 40), _lib.RIB_F32, -1) is None
+
+
+def test_splits_where_they_pay(lib):
+    # 148 SMs, as without a device. Splitting these cost 2.2, 1.5 and 1.1 times the call without it ...
+    n, m = rib.rib_diff_attention_workspace_size, rib.rib_diff_attention_bwd_workspace_size
+    shape = lambda b, q, k, hq, hk, d, dv, **kw: rib.diff_attn_desc(b, q, k, hq, hk, d, dv, 0.25, torch.bfloat16, **kw)  # noqa: E731
+    assert n(shape(1, 1024, 1024, 6, 6, 16, 32)) == 0 and n(shape(32, 1, 1024, 16, 4, 64, 128)) == 0
+    assert m(shape(1, 4096, 4096, 4, 4, 64, 128)) == 4 * 64 * 64 * 60
+    # ... and these gain
+    assert n(shape(16, 1, 8192, 16, 4, 64, 128)) == 2 * 16 * 16 * 2 * 129 * 4
+    assert n(shape(1, 128, 8192, 4, 4, 64, 128)) == 32 * 128 * 4 * 2 * 129 * 4
+    assert m(shape(1, 3000, 200, 2, 1, 32, 64)) == 94 * 64 * 60 + 2 * 11 * 128 * 128 * 4
+    assert m(shape(2, 4001, 4001, 8, 2, 64, 128, causal=True)) == 4 * 252 * 64 * 60 + 128 * 4 * 128 * 256 * 4

@@ -925,17 +925,39 @@ cudaError_t launch_class(const DiffBwdArgs& a, cudaStream_t stream) {
 
 }  // namespace
 
-// Shares of a key tile's rows: one where there are three key tiles an SM;
-// else so many that the longest share is two thirds of an SM's part of all the
-// work, of eight boxes at least.
+// Shares of a key tile's rows, of eight boxes at least; one where there are
+// three key tiles an SM. Measured, in us of a whole backward by the number of shares:
+//   2 x 4001 causal, 8 on 2 heads of 64/128    475 (1)  404 (2)  377 (3)  352 (4)  383 (6)  416 (8)
+//   8192 causal, 2 heads of 32/64              262 (1)  213 (2)  225 (3)  227 (4)  244 (6)
+//   4096 causal, 4 heads of 64/128             170 (1)  172 (2)  168 (3)  176 (4)  207 (6)
+//   4096, the same heads                       172 (1)  197 (2)  211 (3)
+//   3000 on 200 keys, 2 on 1 heads of 32/64    119 (1)  58 (4)  47 (8)  43 (12)
+//   4 x 2048 causal, 8 heads of 32/64          213 (1)  252 (2)
 int diff_bwd_splits(const DiffGeom& g) {
   const long long k_tiles = ceil_div(diff_max_k_boxes(g), 2), boxes = diff_max_q_boxes(g);
   const long long tiles = static_cast<long long>(diff_sequences(g)) * g.kv_heads * k_tiles;
-  if (tiles == 0 || boxes < 16 || tiles >= 3ll * sm_count()) return 1;
-  const long long total = tiles * boxes / (g.causal ? 2 : 1);   // boxes of all tiles
-  const long long want = (3 * boxes * sm_count() + 2 * total - 1) / (2 * total), most = boxes / 8;
-  const long long s = want < most ? want : most;
-  return static_cast<int>(s < 1 ? 1 : (s < 16 ? s : 16));
+  const int sms = sm_count();
+  if (tiles == 0 || boxes < 16 || tiles >= 3ll * sms) return 1;
+  const long long most = boxes / 8 < 16 ? boxes / 8 : 16;
+  if (g.causal) {
+    // the first key tiles have the most rows: so many shares that the longest is two thirds of an SM's part of all the work
+    const long long total = tiles * boxes / 2;
+    const long long want = (3 * boxes * sms + 2 * total - 1) / (2 * total);
+    return static_cast<int>(want < most ? want : most);
+  }
+  // all tiles are alike: the least estimate of time. A box takes a CTA about 1.2 us, its start and end as much as four;
+  // the join 6 us and its sums' bytes, written and read, at 5 TB/s
+  int best = 1;
+  float least = 0.f;
+  for (int s = 1; s <= most; ++s) {
+    const float us = static_cast<float>((tiles * s + sms - 1) / sms) * ((boxes + s - 1) / s + 4) * 1.2f +
+                     (s > 1 ? 6.f + static_cast<float>(tiles * s) * (2 * g.d + g.dv) / 4900.f : 0.f);
+    if (s == 1 || us < least) {
+      least = us;
+      best = s;
+    }
+  }
+  return best;
 }
 
 size_t diff_bwd_part_bytes(const DiffGeom& g) {

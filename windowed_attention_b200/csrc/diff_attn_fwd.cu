@@ -606,24 +606,28 @@ cudaError_t launch_class(const DiffFwdArgs& a, cudaStream_t stream) {
 }  // namespace
 
 // CTAs that share a query tile's keys: the number with the least estimate of
-// (rounds of CTAs) x (boxes of one + 4 for its start and end), of four boxes at
-// least; + 3 for the launch that joins them. Full tiles write and read back as
-// much as four boxes more for each part, and are split only while they leave
-// SMs idle. One CTA a tile of few rows counts half as much again, since the
-// form for few rows joins parts in any case. Measured (16 x 8192 keys, 64 tiles
-// of 4 rows): 65 us with two, 71 with four.
+// time, of four boxes each at least. A key box takes a CTA about 0.75 us, in the
+// form for few rows 0.55; its start and end as much as four; the join 6 us and
+// 4.2 ns a row (a CTA each). Measured, in us by the number of parts:
+//   16 x 1 token, 8192 keys, 16 on 4 heads of 64/128   121 (1)  72 (2)  88 (3)  78 (4)
+//   32 x 1 token, 1024 keys, the same heads             27 (1)  40 (2)  53 (4)
+//   128 tokens, 8192 keys, 4 heads of 64/128           119 (1)  49 (4)  31 (16)  29 (32)  41 (64)
+//   256 tokens, 4096 keys, 8 heads of 64/128            66 (1)  43 (4)  38 (8)  51 (12)
+//   1024 tokens, 1024 keys, 6 heads of 16/32            21 (1)  45 (2)  45 (3)
 int diff_splits(const DiffGeom& g) {
   if (g.window || g.q_len == 0 || g.batch == 0) return 1;
   const bool few = diff_few_rows(g);
   const long long units = static_cast<long long>(g.batch) * g.kv_heads * ceil_div(diff_max_q_boxes(g), 2);
-  const int sms = sm_count(), boxes = ceil_div(g.k_len, kBK), ends = few ? 4 : 8;
+  const int sms = sm_count(), boxes = ceil_div(g.k_len, kBK);
   if (units >= (few ? 4ll : 1ll) * sms) return 1;
+  const auto rounds = [&](int s) { return static_cast<float>((units * s + sms - 1) / sms) * (ceil_div(boxes, s) + 4); };
+  const float join = 6.f + 0.0042f * (static_cast<float>(g.batch) * g.q_heads * g.q_len);
   int best = 1;
-  float least = static_cast<float>((units + sms - 1) / sms) * (boxes + 4) * (few ? 1.5f : 1.f);
-  for (int s = 2; s <= 64 && 4 * s <= boxes; ++s) {
-    const float cost = static_cast<float>((units * s + sms - 1) / sms) * (ceil_div(boxes, s) + ends) + 3;
-    if (cost < least) {
-      least = cost;
+  float least = rounds(1) * 0.75f;
+  for (int s = 2; s <= kMostParts && 4 * s <= boxes; ++s) {
+    const float us = rounds(s) * (few ? 0.55f : 0.75f) + join;
+    if (us < least) {
+      least = us;
       best = s;
     }
   }
