@@ -46,8 +46,8 @@ constexpr int kWarpS = 16, kWarpX = 17, kWarpLoad = 18, kWarpClear = 19;
 constexpr int kThreads = 32 * 20;
 
 enum Site : int {
-  SITE_RAW = 420, SITE_OWN = 421, SITE_ST_FULL = 422, SITE_ST_EMPTY = 423, SITE_S_FULL = 424, SITE_S_FREE = 425, SITE_X_FULL = 426,
-  SITE_X_DONE = 427, SITE_DONE = 428,
+  SITE_RAW = 620, SITE_OWN = 621, SITE_ST_FULL = 622, SITE_ST_EMPTY = 623, SITE_S_FULL = 624, SITE_S_FREE = 625, SITE_X_FULL = 626,
+  SITE_X_DONE = 627, SITE_DONE = 628,
 };
 
 // fp16 probabilities and their gradients are held times 2^6, which moves

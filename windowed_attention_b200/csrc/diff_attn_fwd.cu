@@ -43,7 +43,7 @@ namespace {
 constexpr int kBK = 64;
 
 enum Site : int {
-  SITE_RAW = 400, SITE_Q = 401, SITE_KV_FULL = 402, SITE_KV_EMPTY = 403, SITE_S = 404, SITE_P = 405, SITE_PV = 406, SITE_DONE = 407,
+  SITE_RAW = 600, SITE_Q = 601, SITE_KV_FULL = 602, SITE_KV_EMPTY = 603, SITE_S = 604, SITE_P = 605, SITE_PV = 606, SITE_DONE = 607,
 };
 
 template <int D, int DV>

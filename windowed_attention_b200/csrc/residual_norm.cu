@@ -52,6 +52,8 @@ bool make_drop_rng(float p, uint64_t seed, uint64_t offset, const uint64_t* step
 
 namespace {
 
+enum NormSite : int { SITE_N_FULL = 701 };
+
 constexpr int kMaxC = 4096;
 constexpr int kMaxGroups = 1024;
 constexpr int kSums = 5;   // dscale, dpost_w, dpost_b, dpre_w, dpre_b
@@ -248,7 +250,7 @@ struct BlockIo {
   __device__ __forceinline__ bool ready(int st, long long r0, long long r1, const void* const (&src)[5]) {
     bool ok = true;
     if (whole(r0, r1)) {
-      ok = mbar_wait(&full[st], (laps >> st) & 1u, WaitCtx{abort_flag, p.err}, 501);
+      ok = mbar_wait(&full[st], (laps >> st) & 1u, WaitCtx{abort_flag, p.err}, SITE_N_FULL);
       laps ^= 1u << st;
     } else {
       if (threadIdx.x == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");

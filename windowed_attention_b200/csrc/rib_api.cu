@@ -74,25 +74,42 @@ const char* site_name(int s) {
     case 307: return "attention backward: accumulate MMAs";
     case 308: return "attention backward: final MMA drain";
     case 309: return "attention backward: TMA drain";
-    case 400: return "differential attention: box loaded";
-    case 420: return "differential attention backward: box loaded";
-    case 401: return "differential attention: queries loaded";
-    case 402: return "differential attention: stage loaded";
-    case 403: return "differential attention: free stage";
-    case 404: return "differential attention: S ready";
-    case 405: return "differential attention: P written";
-    case 406: return "differential attention: P V";
-    case 407: return "differential attention: MMA drain";
-    case 421: return "differential attention backward: own tiles";
-    case 422: return "differential attention backward: stage loaded";
-    case 423: return "differential attention backward: free stage";
-    case 424: return "differential attention backward: S ready";
-    case 425: return "differential attention backward: S read";
-    case 426: return "differential attention backward: dS written";
-    case 427: return "differential attention backward: accumulate MMAs";
-    case 428: return "differential attention backward: MMA drain";
-    case 501: return "residual norm: block loaded";
+    case 401: return "fused gate: input stage free";
+    case 402: return "fused gate: input stage loaded";
+    case 403: return "fused gate: depthwise output free";
+    case 404: return "fused gate: depthwise output written";
+    case 405: return "fused gate: accumulator free";
+    case 406: return "fused gate: accumulator ready";
+    case 407: return "fused gate: drain";
+    case 501: return "token backward: raw stage free";
+    case 502: return "token backward: raw stage loaded";
+    case 503: return "token backward: A operand free";
+    case 504: return "token backward: A operand written";
+    case 505: return "token backward: weights free";
+    case 506: return "token backward: weights staged";
+    case 507: return "token backward: accumulator free";
+    case 508: return "token backward: accumulator ready";
+    case 509: return "token backward: drain";
+    case 600: return "differential attention: box loaded";
+    case 620: return "differential attention backward: box loaded";
+    case 601: return "differential attention: queries loaded";
+    case 602: return "differential attention: stage loaded";
+    case 603: return "differential attention: free stage";
+    case 604: return "differential attention: S ready";
+    case 605: return "differential attention: P written";
+    case 606: return "differential attention: P V";
+    case 607: return "differential attention: MMA drain";
+    case 621: return "differential attention backward: own tiles";
+    case 622: return "differential attention backward: stage loaded";
+    case 623: return "differential attention backward: free stage";
+    case 624: return "differential attention backward: S ready";
+    case 625: return "differential attention backward: S read";
+    case 626: return "differential attention backward: dS written";
+    case 627: return "differential attention backward: accumulate MMAs";
+    case 628: return "differential attention backward: MMA drain";
+    case 701: return "residual norm: block loaded";
     case 901: return "self-test wait (nothing arrives)";
+    case 902: return "self-test: MMA rate";
     default: return "unknown";
   }
 }
