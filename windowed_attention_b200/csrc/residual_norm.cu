@@ -780,7 +780,7 @@ int row_unit(int C, int size) {
 
 // CTAs of a group in the backward: two an SM over all groups, no more than the group has rows.
 long long bwd_chunks(long long T, long long rows_per_group, int groups) {
-  const long long chunks = (2ll * 148 + groups - 1) / groups;
+  const long long chunks = (2ll * sm_count() + groups - 1) / groups;
   const long long rows = rows_per_group < T ? rows_per_group : T;
   return chunks < rows ? chunks : (rows > 0 ? rows : 1);
 }
