@@ -83,6 +83,7 @@ constexpr int kInRows = kTY + 2;                      // input rows of a tile (h
 template <int NEPI, int X2, int DW>
 __host__ __device__ constexpr int threads_of() { return (2 + DW + NEPI + X2) * 32; }
 constexpr int kMaxIn = 3;                             // input stages at most
+constexpr int kSmemLimit = 227 * 1024;                // dynamic shared memory at most
 constexpr int kAccCols = 128;                         // one accumulator stage: two M=128 x N=64 tiles
 
 enum FusedGateSite : int {
@@ -589,7 +590,7 @@ cudaError_t launch_dw_pw_fused(const void* X, int B, int H, int W, int Cin, int 
     const int cfg[4][2] = {{3, 2}, {2, 2}, {3, 1}, {2, 1}};
     for (int i = 0; i < 4; ++i) {
       const int tot = up(cfg[i][0] * p.in_stage, 1024) + 2 * p.KA * kTP * 128 + cfg[i][1] * stb + misc_bytes + 1024;
-      if (tot <= 227 * 1024) {
+      if (tot <= kSmemLimit) {
         p.nin = cfg[i][0];
         p.nst = cfg[i][1];
         break;
@@ -601,7 +602,7 @@ cudaError_t launch_dw_pw_fused(const void* X, int B, int H, int W, int Cin, int 
   p.off_st = p.off_d + 2 * p.d_stage;
   p.off_misc = p.off_st + p.nst * p.st_bytes;
   const int total = p.off_misc + misc_bytes + 1024;
-  if (total > 227 * 1024) return cudaErrorInvalidConfiguration;
+  if (total > kSmemLimit) return cudaErrorInvalidConfiguration;
   // depthwise warps: nine for the gate (16 warps in all, 128 registers a
   // thread), six for the ConvFFN, whose eight epilogue warps need the rest
   const int dw_threads = (ffn ? 6 : 9) * 32;
@@ -628,16 +629,17 @@ cudaError_t launch_dw_pw_fused(const void* X, int B, int H, int W, int Cin, int 
                    dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE) != CUDA_SUCCESS)
     return cudaErrorInvalidValue;
   const int grid = p.n_tiles < sm_count() ? p.n_tiles : sm_count();
+  // always the most: the limit is the kernel's, and a call of another host thread may not lower it
   if (ffn) {
-    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<8, 0, 6>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<8, 0, 6>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     cla_gate_fused_kernel<8, 0, 6><<<grid, threads_of<8, 0, 6>(), total, stream>>>(tm, p);
   } else if (p.split == 2) {
-    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<4, 1, 9>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<4, 1, 9>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     cla_gate_fused_kernel<4, 1, 9><<<grid, threads_of<4, 1, 9>(), total, stream>>>(tm, p);
   } else {
-    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<4, 0, 9>, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+    cudaError_t e = cudaFuncSetAttribute(cla_gate_fused_kernel<4, 0, 9>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
     if (e != cudaSuccess) return e;
     cla_gate_fused_kernel<4, 0, 9><<<grid, threads_of<4, 0, 9>(), total, stream>>>(tm, p);
   }

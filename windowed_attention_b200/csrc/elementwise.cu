@@ -251,6 +251,7 @@ constexpr int kPbSub = 32;      // tokens per shared-memory sub-tile
 constexpr int kPbAcc = 64;      // accumulators per thread at most (dWpq, dWpk)
 constexpr int kPbAccE = 32;     // ... (dWh)
 constexpr int kPbThreads = 256;
+constexpr int kPbSmemMost = 200 * 1024;
 constexpr int kPbChunks = 48;   // token chunks (<= kPosBwdChunks, the workspace's partial slots)
 static_assert(kPbChunks <= kPosBwdChunks, "the workspace holds kPosBwdChunks partials");
 
@@ -270,7 +271,7 @@ __host__ __device__ inline int pb_eper(int E, int hidden) { return pb_pad4((E + 
 // unrolled and interleaved)
 __host__ __device__ inline bool pos_bwd_chunk_fits(int E, int hidden, int outs, int M) {
   return (hidden == 64 || hidden == 128) && outs % 16 == 0 && outs <= kPbThreads && pb_kper(hidden, outs) <= kPbAcc &&
-         pb_eper(E, hidden) <= kPbAccE && pos_bwd_chunk_smem(E, hidden, outs, M) <= 200 * 1024;
+         pb_eper(E, hidden) <= kPbAccE && pos_bwd_chunk_smem(E, hidden, outs, M) <= kPbSmemMost;
 }
 
 template <int MT>
@@ -512,7 +513,8 @@ cudaError_t launch_pos_encode_bwd(const rib_mlp_desc& m, int M, const float* dqp
     const int outs = m.heads * m.R;
     const size_t smem = pos_bwd_chunk_smem(E, m.hidden, outs, M);
     auto kern = m.hidden == 128 ? pos_bwd_chunk_kernel<16> : pos_bwd_chunk_kernel<8>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    // always the most: the limit is the kernel's, and a call of another host thread may not lower it
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kPbSmemMost);
     if (e != cudaSuccess) return e;
     // one wave: 48 chunks x 3 output groups, one CTA per SM (the
     // accumulators take the register file)

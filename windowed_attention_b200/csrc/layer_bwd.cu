@@ -304,6 +304,7 @@ __global__ void __launch_bounds__(kThr) dw_dx_kernel(const float* __restrict__ d
 // memory in a fixed order) go to part[block][c][11]; dw_final_kernel adds the
 // blocks in order.
 constexpr int kRedY = 8;
+constexpr int kRedSmemMost = kRedY * 256 * 11 * static_cast<int>(sizeof(float));   // C <= 256
 __global__ void dw_reduce_kernel(const __nv_bfloat16* __restrict__ X, const float* __restrict__ dD,
                                  const __nv_bfloat16* __restrict__ dG, float* __restrict__ part, int B, int H, int W,
                                  int C, int rpb) {
@@ -529,8 +530,9 @@ cudaError_t launch_cla_gate_bwd(const GateBwdLaunch& a, void* ws, cudaStream_t s
   // depthwise weight and bias gradients, dbpw
   const int cq = C / 4;
   const size_t shm = static_cast<size_t>(kRedY) * cq * 4 * 11 * sizeof(float);
+  // always the most: the limit is the kernel's, and a call of another host thread may not lower it
   if (shm > 48 * 1024) {
-    e = cudaFuncSetAttribute(dw_reduce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shm));
+    e = cudaFuncSetAttribute(dw_reduce_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kRedSmemMost);
     if (e != cudaSuccess) return e;
   }
   const long long blocks = red_blocks(a.B, a.H);

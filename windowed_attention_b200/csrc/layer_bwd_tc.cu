@@ -707,7 +707,8 @@ cudaError_t launch_gemm(int mode, TcBwdParams p, const CUtensorMap* g, const CUt
   if (total > kSmemLimit) return cudaErrorInvalidConfiguration;
   if (p.n_tiles == 0) return cudaSuccess;
   auto kern = mode == 0 ? tc_bwd_gemm_kernel<0> : tc_bwd_gemm_kernel<1>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+  // always the most: the limit is the kernel's, and a call of another host thread may not lower it
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   const long long grid = p.n_tiles < sm_count() ? p.n_tiles : sm_count();
   kern<<<static_cast<unsigned>(grid), kThreads, total, stream>>>(g[0], g[1], g[2], out_map, p);
@@ -746,7 +747,7 @@ cudaError_t launch_wgrad(int mode, TcBwdParams p, const CUtensorMap* g, int* chu
   *chunks_out = chunks;
   if (p.n_tiles == 0) return cudaSuccess;
   auto kern = mode == 0 ? tc_bwd_wgrad_kernel<0> : tc_bwd_wgrad_kernel<1>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   dim3 grid(chunks, jobs);
   kern<<<grid, kThreads, total, stream>>>(g[0], g[1], g[2], p);

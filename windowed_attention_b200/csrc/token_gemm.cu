@@ -725,7 +725,8 @@ cudaError_t launch_token_gemm(const GemmLaunch& g, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     }
   }
-  cudaError_t e = cudaFuncSetAttribute(rib_token_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, total);
+  // always the most: the limit is the kernel's, and a call of another host thread may not lower it
+  cudaError_t e = cudaFuncSetAttribute(rib_token_gemm_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit);
   if (e != cudaSuccess) return e;
   // one CTA per SM; the persistent grid is co-resident
   const int sms = sm_count();
