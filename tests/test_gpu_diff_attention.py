@@ -569,3 +569,21 @@ def test_a_bad_window_stays_in_its_window_at_wide_heads(cuda_lib, d, dv):
         assert torch.equal(one[k][0, ~bad], two[k][0, ~bad]), k
         assert torch.isnan(two[k][0, bad]).all(), k
     assert torch.equal(one["lse"][..., ~bad], two["lse"][..., ~bad])
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("B,Nq,Nk,Hq,Hk,d,dv,kw", [
+    (2, 150, 190, 2, 2, 16, 32, {}), (2, 150, 190, 4, 2, 64, 128, {"causal": True}), (2, 3, 4099, 8, 2, 64, 128, {}), (1, 70, 6000, 1, 1, 32, 64, {}),
+    (2, 35 * 22, 35 * 22, 2, 1, 24, 40, {"window": 16, "width": 22})], ids=["two-groups", "one-group", "few-rows", "split", "windows"])
+def test_a_bad_query_spoils_its_row_in_every_form(cuda_lib, B, Nq, Nk, Hq, Hk, d, dv, kw, t):
+    """A NaN query makes its row of o NaN, in either map, and leaves every other row's bits."""
+    x = _inputs(B, Nq, Nk, Hq, Hk, d, dv, t)
+    one = _run(cuda_lib, x, 0.125, t, train=False, **kw)["o"]
+    rows = [(0, Nq // 2, 0), (B - 1, Nq - 1, Hq - 1)]
+    for k, (b, n, h) in zip(("q1", "q2"), rows):
+        x[k][b, n, h, d - 1] = float("nan")
+    two = _run(cuda_lib, x, 0.125, t, train=False, **kw)["o"]
+    bad = torch.zeros(B, Nq, Hq, dtype=torch.bool, device="cuda")
+    for r in rows:
+        bad[r] = True
+    assert torch.isnan(two[bad]).all() and torch.equal(one[~bad], two[~bad])
