@@ -491,7 +491,9 @@ rib_status rib_residual_norm_bwd(const rib_residual_norm_desc* desc, const void*
 /* Differential attention: per sequence and query head h, with its key head,
  *   O = (softmax(scale Q1 K1^T) - lam[h] softmax(scale Q2 K2^T)) V
  * Tensors are [batch][tokens][heads][width] with the widths contiguous.
- * Query heads h * (q_heads / kv_heads) .. share key head h. A sequence is a
+ * Query heads h * (q_heads / kv_heads) .. share key head h. A position term of
+ * rank R (scores scale q k^T + qp kp^T) is R more columns: [q, qp / scale] and
+ * [k, kp] as the queries and keys of both maps, d + R <= 64. A sequence is a
  * batch item, or with window > 0 one window x window cell of each item's map
  * [height][width] (q_len = k_len = height * width, cells at the right and
  * lower edge are cut off there). */

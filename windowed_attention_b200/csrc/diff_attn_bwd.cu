@@ -10,6 +10,8 @@
 //
 // Three launches:
 //  * rows: D_1, D_2 and the other row constants, box by box of 64 query rows.
+//    D comes from the stored O and O_2 in their 16-bit type, half a step of each
+//    term, in place of a sum over the keys of P dP (a pass more over the scores).
 //  * dq: one CTA owns 128 query rows and streams key boxes of 64. It also sums
 //    P_2 dP in fp32, which spares dlambda the rounding of a stored O_2.
 //  * dkv: one CTA owns 128 keys of a key head and streams query boxes, keys in

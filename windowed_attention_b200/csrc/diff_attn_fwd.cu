@@ -6,8 +6,10 @@
 // and sum l, O_i accumulates 2^(s' S_i - m_i) V (s' = s log2 e) and the output
 // is O_1 / l_1 - lambda O_2 / l_2, formed once at the end. The maximum is
 // raised (and O_i scaled) only when a tile exceeds it by 2^8, so P <= 256.
-// P takes the 16-bit type for its product with V (half a step of each term);
-// scores, sums and both O_i stay fp32.
+// P takes the 16-bit type for its product with V (half a step of each term, the
+// operand type of one product instead of the two that P in two terms would
+// take: in bf16 the output is 0.0025 of its norm off, 0.0017 of which rounding
+// the result alone takes); scores, sums and both O_i stay fp32.
 //
 // One CTA owns 128 query rows and streams key tiles of 64; V is loaded once
 // for both maps. S of each map has two buffers in TMEM, so the products of the
@@ -29,7 +31,10 @@
 // takes 1024 cycles of the SM's MUFU, of which the FMA pipe takes over POLY of
 // every 8 pairs. Its products take 2 (48 D / 16 + 4 max(DV / 2, 32 + DV / 4)) cycles.
 // Measured: 320x180 map, window 64, 6 heads of 16/32: 860 us, MUFU 82 % busy
-// (floor 596 us). Causal 2x4001 tokens, 8 query on 2 key heads of 64/128: 133 us,
+// (floor 596 us); windows of 32, 16 and 8 320, 182 and 261 us (floors 151, 39
+// and 14: a CTA takes all of TMEM, so nothing hides its start, and its lanes are
+// half empty at 8). Heads of 32/64 913 us, of 48/32, in the tiles of 64/128, 1059.
+// Causal 2x4001 tokens, 8 query on 2 key heads of 64/128: 133 us,
 // bound by the chain of product, softmax and product with two tiles in flight
 // (four softmax groups that share one reference a map: 129 us there, but 2 %
 // more for single tokens; not kept).

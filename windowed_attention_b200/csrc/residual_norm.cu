@@ -23,10 +23,15 @@
 // registers (mean, then squared deviations: no cancellation), and the backward
 // recomputes them from x' and y rather than reading saved ones.
 //
-// Measured: 640x360 rows of 180, fp32 stream, bf16 branch and gate, forward 112
-// us (581 MB, 5.2 TB/s); 16x96x96 rows of 180 with dropout, forward 105 and
-// backward 193 us (floors 57 and 89); 4039 rows of 1021 in fp16, 48 and 81 us
-// (floors 9 and 14). What is above the floors is instruction issue.
+// Measured: 640x360 rows of 180, fp32 stream, bf16 branch and gate, forward
+// 112-118 us by box (581 MB, 4.9-5.2 TB/s); 16x96x96 rows of 180 with dropout,
+// forward 108 and backward 193 us (floors 57 and 89); 4039 rows of 1021 in fp16,
+// forward and backward 131-134 us (floor 23). The forward issues in 68 % of its
+// cycles, between the barriers of 16-row blocks. The backward (149 instructions
+// a warp-wide element, 110 us of issue) issues in 60 %: 15 warps an SM, at 128
+// registers, wait for dependent instructions, shared memory and a block's
+// barriers. Rows of 1021 take pairs with 150 bytes of spills and 65 KB blocks,
+// too large for a second stage, so that loads and arithmetic take turns.
 //
 // Column sums (weights, scale) of the backward: every thread keeps its own
 // columns' sums in fp32 registers over the rows that its group walks; the
